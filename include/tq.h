@@ -383,6 +383,121 @@ tq_status tq_selftest_wait_timeout(tq_ctx *ctx, uint32_t timeout_us, void *strea
 /* Zero the status word (enqueued on `stream`). */
 tq_status tq_reset_status(tq_ctx *ctx, void *stream);
 
+/* ------------------------------------------------------------------------
+ * A paged cache held in 4 bits (the pages have no counterpart).  For serving
+ * loops that keep many sequences of unlike lengths: keys and values of every
+ * sequence live in pages of a common pool, are quantised as they are written
+ * (no rotation, no sketch, no tables: one pass), and are read back or
+ * attended to through a table of page numbers.
+ *
+ * Packed format, 4.25 bits per value.  A head vector is cut into groups of 32
+ * channels.  A group's scale s is one byte b, the binary16 number with the
+ * bits b << 7 (five exponent, three mantissa bits): the smallest with
+ * max|x| <= 7.5 s, at most 7680 (b = 223).  A value is kept as
+ * c = sign(x) floor(|x| / s + 1/2), held to [-8, 7], and stands for c s:
+ * |x - c s| <= s / 2 while max|x| <= 57600, beyond which values saturate.
+ * c s is exact in binary16, bfloat16 and float32.  A row (one head vector)
+ * with a value that is not finite is kept as zeros and counted in the status
+ * word.  A page of one kv head is page_size * (d/2 + d/32) bytes: the codes
+ * [page_size][d/2], c + 8 of channel j in nibble j % 2 of byte j / 2, then
+ * the scale bytes [page_size][d/32].
+ *
+ * The conventions at the top of this file hold.  A handle may be used from
+ * several host threads at once, and by calls on several streams: it holds no
+ * state but the status word.  Calls that touch the same pages, outputs or
+ * workspace at once must be ordered by the caller.  All calls may be captured
+ * into graphs, except tq_paged_create, tq_paged_destroy and
+ * tq_paged_get_status. */
+typedef struct tq_paged tq_paged;
+
+/* The pool: two device buffers laid out [n_pages][n_kv_heads] pages of
+ * tq_paged_page_bytes, 16-byte aligned.  Either may be NULL when the call
+ * does not touch it.  Token t of page p is slot p * page_size + t. */
+typedef struct tq_pages {
+    void *k;
+    void *v;
+    int64_t n_pages;
+    int32_t n_kv_heads;
+    int32_t reserved;
+} tq_pages;
+
+#define TQ_MAX_PAGED_SEQS 65535
+
+/* head_dim in {64, 128, 256} (TQ_ERR_DIM), page_size a power of two in
+ * [16, 256] (TQ_ERR_DIM_MISMATCH), on the current device.  Synchronous. */
+tq_status tq_paged_create(int head_dim, int page_size, tq_paged **out);
+void tq_paged_destroy(tq_paged *ctx);
+
+/* Bytes of one page of one kv head in either buffer (0 for NULL). */
+int64_t tq_paged_page_bytes(const tq_paged *ctx);
+
+/* Quantise rows into the cache.
+ *  k, v     : device rows, element (token i, head h, channel j) at
+ *             i * stride_?t + h * stride_?h + j (in elements); row starts
+ *             16-byte aligned.  Either may be NULL.
+ *  slots    : device int64 [n_tokens].  A negative slot: the row is not kept
+ *             (padding).  A slot past the pool: not kept either, and error
+ *             flag bit 1 is set in the status word.  The kept slots of one
+ *             call must differ (else the slot holds a mixture of the rows).
+ *  k_stored, v_stored : NULL, or device [n_tokens][n_kv_heads][d] in `dtype`,
+ *             contiguous, 16-byte aligned: the values that the format keeps
+ *             for every row (those with a negative slot too).
+ * One kernel. */
+tq_status tq_paged_write(tq_paged *ctx, const void *k, const void *v, tq_dtype dtype, int64_t n_tokens,
+                         int64_t stride_kt, int64_t stride_kh, int64_t stride_vt, int64_t stride_vh,
+                         const int64_t *slots, const tq_pages *pages, void *k_stored, void *v_stored, void *stream);
+
+/* Read rows back: k_out, v_out device [n_tokens][n_kv_heads][d] in `dtype`,
+ * contiguous, 16-byte aligned; either may be NULL.  A slot that is negative
+ * or past the pool (flagged) gives rows of zeros.  One kernel. */
+tq_status tq_paged_read(tq_paged *ctx, const tq_pages *pages, const int64_t *slots, int64_t n_tokens, void *k_out,
+                        void *v_out, tq_dtype dtype, void *stream);
+
+/* Attention over the cache.  Sequence b has seq_lens[b] tokens in the cache,
+ * token t in page page_table[b * table_stride + t / page_size]; its queries
+ * are rows [q_starts[b], q_starts[b + 1]) of q and belong to its last tokens:
+ * query i of n is at position p = seq_lens[b] - n + i, and sees
+ *   t <= p, and, where window > 0, only t > p - window or t < sinks
+ * (a sliding window and a few first tokens that stay visible).
+ *   out = sum_t softmax_t(scale q . k_t) v_t,  zeros where nothing is seen.
+ *  q, out     : device, binary16 or bfloat16 (`dtype`; the scores and sums are
+ *               float32, the weights binary16, the products exact), element
+ *               (row i, head j, channel c) at i * stride_?t + j * stride_?h + c;
+ *               strides multiples of 8 elements, bases 16-byte aligned.  Query
+ *               head j reads kv head j / (n_q_heads / n_kv_heads).  out must
+ *               not overlap q.  Rows of `out` outside every sequence are left
+ *               as they were.
+ *  page_table : device int32, table_stride >= max_pages entries a sequence;
+ *               entries past a sequence's length are not read.
+ *  seq_lens   : device int32 [batch].
+ *  q_starts   : device int32 [batch + 1], or NULL: one query per sequence
+ *               (total_q == batch).
+ *  max_q_len  : the most queries of a sequence, as far as the host knows: the
+ *               choice of kernel and the workspace go by it; more queries
+ *               than that are still answered.
+ *  window     : 0 for none.   scale : 0 for 1/sqrt(d).
+ *  workspace  : >= tq_paged_workspace_bytes(...), 16-byte aligned; contents on
+ *               entry are ignored.
+ * Tokens past a sequence's length may hold anything.  A length outside
+ * [0, max_pages * page_size], a query start outside [0, total_q] or a
+ * decreasing one is held to those bounds, tokens of a page number outside the
+ * pool are not seen, and each sets error flag bit 1 in the status word.
+ * n_q_heads <= TQ_MAX_HEADS, batch <= TQ_MAX_PAGED_SEQS, and total_q *
+ * n_q_heads and max_pages * page_size below 2^30 (TQ_ERR_LIMIT).  At most two
+ * kernels, the second a programmatic dependent launch. */
+size_t tq_paged_workspace_bytes(const tq_paged *ctx, int n_q_heads, int n_kv_heads, int batch, int64_t max_pages,
+                                int max_q_len);
+tq_status tq_paged_attention(tq_paged *ctx, const tq_pages *pages, const void *q, tq_dtype dtype, int64_t total_q,
+                             int n_q_heads, int64_t stride_qt, int64_t stride_qh, const int32_t *page_table,
+                             int64_t table_stride, int64_t max_pages, const int32_t *seq_lens, const int32_t *q_starts,
+                             int batch, int max_q_len, int window, int sinks, float scale, void *out,
+                             int64_t stride_ot, int64_t stride_oh, void *workspace, size_t ws_bytes, void *stream);
+
+/* As tq_get_status and tq_reset_status; flag bit 1: a slot, page number,
+ * length or query start was out of range. */
+tq_status tq_paged_get_status(tq_paged *ctx, void *stream, uint64_t *nonfinite_rows, uint32_t *error_flags);
+tq_status tq_paged_reset_status(tq_paged *ctx, void *stream);
+
 /* Human-readable name of a status code (static storage). */
 const char *tq_status_string(tq_status s);
 

@@ -15,6 +15,7 @@ Names follow the C ABI (``tq_create``, ``tq_encode_kv``,
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -40,7 +41,9 @@ EXPORTED = ["tq_create", "tq_create_ex", "tq_create_format", "tq_destroy", "tq_e
             "tq_decode_attention",
             "tq_get_status", "tq_reset_status", "tq_status_string", "tq_last_cuda_error",
             "tq_decode_attention_static", "tq_decode_append", "tq_decode_append_workspace_bytes",
-            "tq_selftest_wait_timeout", "tq_decode_attention_split", "tq_decode_split_workspace_bytes"]
+            "tq_selftest_wait_timeout", "tq_decode_attention_split", "tq_decode_split_workspace_bytes",
+            "tq_paged_create", "tq_paged_destroy", "tq_paged_page_bytes", "tq_paged_write", "tq_paged_read",
+            "tq_paged_workspace_bytes", "tq_paged_attention", "tq_paged_get_status", "tq_paged_reset_status"]
 
 
 class TQError(RuntimeError):
@@ -61,6 +64,11 @@ class tq_segment(ctypes.Structure):
     _fields_ = [("ctx", ctypes.c_void_p), ("codes", tq_codes), ("codes_batch", ctypes.c_int32),
                 ("first_seq", ctypes.c_int32), ("n_seqs", ctypes.c_int32), ("reserved", ctypes.c_int32),
                 ("n_tokens", ctypes.c_int64)]
+
+
+class tq_pages(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("n_pages", ctypes.c_int64),
+                ("n_kv_heads", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 def _load():
@@ -91,6 +99,16 @@ def _load():
         "tq_decode_split_workspace_bytes": (SZ, [V, V, I, I, I64]),
         "tq_decode_attention_split": (I, [V, ctypes.POINTER(tq_codes), V, ctypes.POINTER(tq_codes), I64, V, I, I, I,
                                           V, I, V, SZ, V]),
+        "tq_paged_create": (I, [I, I, ctypes.POINTER(V)]),
+        "tq_paged_destroy": (None, [V]),
+        "tq_paged_page_bytes": (I64, [V]),
+        "tq_paged_write": (I, [V, V, V, I, I64, I64, I64, I64, I64, V, ctypes.POINTER(tq_pages), V, V, V]),
+        "tq_paged_read": (I, [V, ctypes.POINTER(tq_pages), V, I64, V, V, I, V]),
+        "tq_paged_workspace_bytes": (SZ, [V, I, I, I, I64, I]),
+        "tq_paged_attention": (I, [V, ctypes.POINTER(tq_pages), V, I, I64, I, I64, I64, V, I64, I64, V, V, I, I, I, I,
+                                   ctypes.c_float, V, I64, I64, V, SZ, V]),
+        "tq_paged_get_status": (I, [V, V, ctypes.POINTER(ctypes.c_uint64), ctypes.POINTER(ctypes.c_uint32)]),
+        "tq_paged_reset_status": (I, [V, V]),
         "tq_status_string": (ctypes.c_char_p, [I]),
         "tq_last_cuda_error": (ctypes.c_char_p, []),
     }
@@ -447,3 +465,186 @@ class KvCache:
 
     def clear(self):
         self._len = 0
+
+
+class PagedCache:
+    """A paged cache held in 4 bits (include/tq.h, "A paged cache held in 4
+    bits"): a pool of pages shared by many sequences, written with
+    quantisation, read back, and attended to through a page table, with an
+    optional sliding window and a few first tokens that stay visible.
+
+    k, v: the pool, uint8 [n_pages, n_kv_heads, page bytes].  Token t of page
+    p is slot p * page_size + t.  Calls run on the cache's device, on
+    `stream` or else on that device's current stream; their tensors must be
+    on that device."""
+
+    def __init__(self, n_pages: int, n_kv_heads: int, head_dim: int, page_size: int = 64, device="cuda"):
+        import torch
+        self.ctx = None
+        if n_pages <= 0 or n_kv_heads <= 0:
+            raise TQError(7, "PagedCache")                   # TQ_ERR_EMPTY
+        device = torch.device(device)
+        self.device = torch.device("cuda", torch.cuda.current_device() if device.index is None else device.index)
+        self.n_pages, self.n_kv_heads, self.head_dim, self.page_size = n_pages, n_kv_heads, head_dim, page_size
+        self._codes = {torch.float32: TQ_F32, torch.float16: TQ_F16, torch.bfloat16: TQ_BF16}
+        out = ctypes.c_void_p()
+        with torch.cuda.device(self.device):
+            _check(_lib.tq_paged_create(head_dim, page_size, ctypes.byref(out)), "tq_paged_create")
+        self.ctx = out.value
+        self.page_bytes = _lib.tq_paged_page_bytes(self.ctx)
+        self.k = torch.zeros(n_pages, n_kv_heads, self.page_bytes, dtype=torch.uint8, device=self.device)
+        self.v = torch.zeros_like(self.k)
+
+    def close(self):
+        if self.ctx:
+            _lib.tq_paged_destroy(self.ctx)
+            self.ctx = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def struct(self) -> tq_pages:
+        return tq_pages(self.k.data_ptr(), self.v.data_ptr(), self.n_pages, self.n_kv_heads, 0)
+
+    def _on(self, stream):
+        """Makes `stream` and the cache's device current, where they are not."""
+        import torch
+        if stream is None:
+            if torch.cuda.current_device() == self.device.index:
+                return contextlib.nullcontext()
+            return torch.cuda.device(self.device)
+        if stream.device != self.device:
+            raise TQError(12, "PagedCache")                  # TQ_ERR_DEVICE
+        return torch.cuda.stream(stream)
+
+    def _want(self, where: str, *tensors):
+        for t in tensors:
+            if t is not None and t.device != self.device:
+                raise TQError(12, where)                     # TQ_ERR_DEVICE
+
+    def _rows(self, t):
+        """Rows as the library takes them: contiguous channels, 16-byte aligned starts (else a copy)."""
+        sx, sh, sd = t.stride()
+        if sd == 1 and not (sx | sh) * t.element_size() % 16 and t.data_ptr() % 16 == 0:
+            return t
+        return t.clone() if t.is_contiguous() else t.contiguous()
+
+    def write(self, k, v, slots, stored: bool = False, stream=None):
+        """Quantise rows k, v [n_tokens, n_kv_heads, head_dim] (float32,
+        float16 or bfloat16; either may be None) into `slots` (int64
+        [n_tokens]; a negative slot is padding; the others must differ).
+        With `stored`, returns the values that the cache keeps for them, in
+        the rows' type (None for a None)."""
+        import torch
+        ref = k if k is not None else v
+        if ref is None:
+            raise TQError(1, "PagedCache.write")             # TQ_ERR_NULL
+        n, code = ref.shape[0] if ref.dim() else 0, self._codes.get(ref.dtype)
+        for t in (k, v):
+            if t is not None and (t.dtype != ref.dtype or t.shape != (n, self.n_kv_heads, self.head_dim)):
+                raise TQError(8, "PagedCache.write")         # TQ_ERR_DIM_MISMATCH
+        if code is None or slots.dtype != torch.int64 or slots.shape != (n,):
+            raise TQError(8, "PagedCache.write")
+        self._want("PagedCache.write", k, v, slots)
+        with self._on(stream):
+            slots = slots.contiguous()
+            ks = vs = None
+            pk = pv = pks = pvs = None
+            sk = sv = (0, 0, 0)
+            if k is not None:
+                k = self._rows(k)
+                pk, sk = k.data_ptr(), k.stride()
+                if stored:
+                    ks = torch.empty(k.shape, dtype=k.dtype, device=self.device)
+                    pks = ks.data_ptr()
+            if v is not None:
+                v = self._rows(v)
+                pv, sv = v.data_ptr(), v.stride()
+                if stored:
+                    vs = torch.empty(v.shape, dtype=v.dtype, device=self.device)
+                    pvs = vs.data_ptr()
+            c = self.struct()
+            _check(_lib.tq_paged_write(self.ctx, pk, pv, code, n, sk[0], sk[1], sv[0], sv[1], slots.data_ptr(),
+                                       ctypes.byref(c), pks, pvs, _stream()), "tq_paged_write")
+        return (ks, vs) if stored else None
+
+    def read(self, slots, dtype=None, keys: bool = True, values: bool = True, stream=None):
+        """The rows at `slots` (int64 [n_tokens]) as (k, v), each [n_tokens,
+        n_kv_heads, head_dim] in `dtype` (default bfloat16; None for one not
+        asked for); a negative slot gives zeros."""
+        import torch
+        dtype = dtype or torch.bfloat16
+        code = self._codes.get(dtype)
+        if code is None or slots.dim() != 1 or slots.dtype != torch.int64:
+            raise TQError(8, "PagedCache.read")
+        self._want("PagedCache.read", slots)
+        with self._on(stream):
+            slots = slots.contiguous()
+            shape = (slots.shape[0], self.n_kv_heads, self.head_dim)
+            kh = torch.empty(shape, dtype=dtype, device=self.device) if keys else None
+            vh = torch.empty(shape, dtype=dtype, device=self.device) if values else None
+            c = self.struct()
+            _check(_lib.tq_paged_read(self.ctx, ctypes.byref(c), slots.data_ptr(), shape[0],
+                                      kh.data_ptr() if keys else None, vh.data_ptr() if values else None, code,
+                                      _stream()), "tq_paged_read")
+        return kh, vh
+
+    def workspace_bytes(self, n_q_heads: int, batch: int, max_pages: int, max_q_len: int = 1) -> int:
+        return _lib.tq_paged_workspace_bytes(self.ctx, n_q_heads, self.n_kv_heads, batch, max_pages, max_q_len)
+
+    def attention(self, q, page_table, seq_lens, q_starts=None, max_q_len=None, window: int = 0, sinks: int = 0,
+                  scale=None, out=None, workspace=None, stream=None):
+        """Attention of the last tokens of each sequence over its cached
+        tokens, causal.  q: [total_q, n_q_heads, head_dim] float16 or
+        bfloat16; page_table: int32 [batch, max_pages]; seq_lens: int32
+        [batch]; q_starts: int32 [batch + 1], the first query of each sequence
+        and the end (None: one query per sequence); max_q_len: the most
+        queries of a sequence (default 1 without q_starts, else total_q);
+        window: 0, or how many tokens back a query sees besides the first
+        `sinks`; scale: default 1/sqrt(head_dim).  Returns `out` (like q;
+        rows of no sequence are not written)."""
+        import torch
+        i32 = torch.int32
+        if q.dim() != 3 or page_table.dim() != 2 or q.dtype == torch.float32 or q.dtype not in self._codes:
+            raise TQError(8, "PagedCache.attention")
+        (total, heads, d), (batch, pages) = q.shape, page_table.shape
+        if (d != self.head_dim or page_table.dtype != i32 or seq_lens.dtype != i32 or seq_lens.shape != (batch,) or
+                (q_starts is not None and (q_starts.dtype != i32 or q_starts.shape != (batch + 1,))) or
+                (out is not None and (out.shape != q.shape or out.dtype != q.dtype or out.stride(2) != 1))):
+            raise TQError(8, "PagedCache.attention")
+        self._want("PagedCache.attention", q, page_table, seq_lens, q_starts, out, workspace)
+        most = max_q_len or (1 if q_starts is None else max(total, 1))
+        with self._on(stream):
+            q, seq_lens = self._rows(q), seq_lens.contiguous()
+            if page_table.stride(1) != 1 or page_table.stride(0) < pages:
+                page_table = page_table.contiguous()
+            if q_starts is not None:
+                q_starts = q_starts.contiguous()
+            if out is None:
+                out = torch.empty(total, heads, d, dtype=q.dtype, device=self.device)
+            if workspace is None:
+                need = self.workspace_bytes(heads, batch, pages, most)
+                workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
+            (sqt, sqh, _), (sot, soh, _) = q.stride(), out.stride()
+            c = self.struct()
+            _check(_lib.tq_paged_attention(
+                self.ctx, ctypes.byref(c), q.data_ptr(), self._codes[q.dtype], total, heads, sqt, sqh,
+                page_table.data_ptr(), max(page_table.stride(0), pages), pages, seq_lens.data_ptr(),
+                None if q_starts is None else q_starts.data_ptr(), batch, most, window, sinks, scale or 0.0,
+                out.data_ptr(), sot, soh, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                _stream()), "tq_paged_attention")
+        return out
+
+    def status(self, stream=None):
+        """(rows not finite so far, error flags); synchronises the stream."""
+        n, f = ctypes.c_uint64(), ctypes.c_uint32()
+        with self._on(stream):
+            _check(_lib.tq_paged_get_status(self.ctx, _stream(), ctypes.byref(n), ctypes.byref(f)), "tq_paged_get_status")
+        return n.value, f.value
+
+    def reset_status(self, stream=None):
+        with self._on(stream):
+            _check(_lib.tq_paged_reset_status(self.ctx, _stream()), "tq_paged_reset_status")

@@ -1,0 +1,566 @@
+// tq_paged.cu -- the paged 4-bit cache: handle, argument checks, and the two
+// kernels that write rows into pages and read rows back (tq_paged.cuh gives
+// the format; the attention kernels are in tq_paged_attend.cu).
+//
+// Both kernels move bytes: 4.25 bits of packed row against 16 (or 32) bits of
+// plain value, a dozen instructions for each value.  A thread owns eight
+// consecutive channels of a row, one 16-byte load (binary16, bfloat16) and
+// one 4-byte word of codes, so a warp reads and writes whole sectors; four
+// lanes share a scale.
+#include <climits>
+#include <cmath>
+#include <cstring>
+#include <new>
+
+#include "tq_paged.cuh"
+
+int tq_device_sms(int dev);
+
+namespace {
+
+constexpr int RW_THREADS = 256;
+
+struct RowsArg {
+    const void *k, *v;          // plain rows in (write)
+    void *ko, *vo;              // plain rows out (read; stored values of a write), contiguous
+    uint8_t *kc, *vc;           // pages
+    const int64_t *slots;
+    int64_t skt, skh, svt, svh; // element strides of k and v: token, head
+    int64_t n_rows;             // tokens * heads
+    int64_t n_slots, page_bytes;
+    uint64_t inv_H;             // ceil(2^32 / H): r / H for r < 2^16
+    int H, lg_page;
+    unsigned long long *status;
+};
+
+__device__ __forceinline__ float scale_value(uint32_t byte) {
+    return __half2float(__ushort_as_half((unsigned short)(byte << 7)));
+}
+
+// The smallest scale byte with amax <= 7.5 s.  7.5 times a scale has eight
+// bits, so the comparison is exact; the quotient is only a first guess, made
+// a little too small (at most one step for values of up to eleven bits,
+// two for float32).
+__device__ __forceinline__ uint32_t scale_byte(float amax) {
+    const float y = amax * (0.13333333f * (1.f - 1.f / 1048576.f));
+    uint32_t b = y < 6.103515625e-05f ? (uint32_t)(y * 131072.f) : (__float_as_uint(y) >> 20) - 896u;
+    b = min(b, PG_MAX_SCALE);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        if (b < PG_MAX_SCALE && 7.5f * scale_value(b) < amax) ++b;
+    return b;
+}
+
+template <typename T>
+struct Eight;   // eight plain values: load, |max| with a test for finite, store
+
+template <>
+struct Eight<float> {
+    float x[8];
+    __device__ __forceinline__ void load(const float *p) {
+        const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = 0.f;
+    }
+    // bits of the largest magnitude: not finite if >= LIMIT
+    static constexpr uint32_t LIMIT = 0x7F800000u;
+    __device__ __forceinline__ uint32_t amax_bits() const {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+        return m;
+    }
+    static __device__ __forceinline__ float from_bits(uint32_t b) { return __uint_as_float(b); }
+    __device__ __forceinline__ float get(int i) const { return x[i]; }
+    static __device__ __forceinline__ void store(float *p, const float (&v)[8]) {
+        reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    }
+};
+
+template <typename T>
+struct Eight16 {
+    uint4 w;
+    __device__ __forceinline__ void load(const T *p) { w = __ldg(reinterpret_cast<const uint4 *>(p)); }
+    __device__ __forceinline__ void zero() { w = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ uint32_t amax_bits() const {
+        uint32_t m = __vmaxu2(__vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu),
+                              __vmaxu2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu));
+        return max(m >> 16, m & 0xFFFFu);
+    }
+    __device__ __forceinline__ uint32_t half_word(int i) const {
+        const uint32_t x = i < 2 ? w.x : i < 4 ? w.y : i < 6 ? w.z : w.w;
+        return (i & 1) ? x >> 16 : x & 0xFFFFu;
+    }
+};
+
+template <>
+struct Eight<__half> : Eight16<__half> {
+    static constexpr uint32_t LIMIT = 0x7C00u;
+    static __device__ __forceinline__ float from_bits(uint32_t b) { return __half2float(__ushort_as_half((unsigned short)b)); }
+    __device__ __forceinline__ float get(int i) const { return from_bits(half_word(i)); }
+    static __device__ __forceinline__ void store(__half *p, const float (&v)[8]) {
+        uint32_t o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+            o[i] = *reinterpret_cast<const uint32_t *>(&h);
+        }
+        *reinterpret_cast<uint4 *>(p) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+};
+
+template <>
+struct Eight<__nv_bfloat16> : Eight16<__nv_bfloat16> {
+    static constexpr uint32_t LIMIT = 0x7F80u;
+    static __device__ __forceinline__ float from_bits(uint32_t b) { return __uint_as_float(b << 16); }
+    __device__ __forceinline__ float get(int i) const {
+        const uint32_t x = i < 2 ? w.x : i < 4 ? w.y : i < 6 ? w.z : w.w;
+        return __uint_as_float((i & 1) ? x & 0xFFFF0000u : x << 16);
+    }
+    static __device__ __forceinline__ void store(__nv_bfloat16 *p, const float (&v)[8]) {
+        uint32_t o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+            o[i] = *reinterpret_cast<const uint32_t *>(&h);
+        }
+        *reinterpret_cast<uint4 *>(p) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+};
+
+// Where a thread's eight channels of row `row` are.
+struct Place {
+    int64_t token;
+    int head;
+};
+
+__device__ __forceinline__ Place place_of(const RowsArg &A, int64_t base_token, int base_head, int local) {
+    const uint32_t r = (uint32_t)(base_head + local);   // < H + rows of a block < 2^16
+    const uint32_t t = (uint32_t)(((uint64_t)r * A.inv_H) >> 32);
+    return {base_token + t, (int)(r - t * (uint32_t)A.H)};
+}
+
+// Quantise one thread's eight values (four lanes share a group, D / 8 a row)
+// and store codes, scale and, if `so`, the stored values.
+template <typename T, int D>
+__device__ __forceinline__ void quantise_store(Eight<T> x, bool live, bool kept, uint8_t *page, int t, int lg_page, int j,
+                                               T *so, unsigned &bad_rows) {
+    constexpr int LANES = D / 8;
+    const int lane = threadIdx.x & 31;
+    uint32_t m = x.amax_bits();
+    // a row with a value that is not finite is stored as zeros
+    const uint32_t row_mask = (uint32_t)(((1ull << LANES) - 1) << (lane & ~(LANES - 1)));
+    const bool bad = (__ballot_sync(0xffffffffu, m >= Eight<T>::LIMIT) & row_mask) != 0;
+    if (bad) {
+        x.zero();
+        m = 0;
+        if (live && j == 0) ++bad_rows;
+    }
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    const uint32_t byte = scale_byte(Eight<T>::from_bits(m));
+    const float s = scale_value(byte);
+    // Rounding by a first product: x / s of a value with at most 11 bits is
+    // either a half-way point n + 1/2 or at least 2^-12 of itself away from
+    // one (s has four bits), so a reciprocal made 2^-16 too large rounds
+    // half-way points away from zero and moves nothing else.  A float32 value
+    // is compared with (n +- 1/2) s, which is exact.
+    const float inv = byte ? __fdividef(1.f, s) * (1.f + 1.f / 65536.f) : 0.f;
+    constexpr float MAGIC = 12582920.f;   // 1.5 * 2^23 + 8: the sum's low bits are the code + 8
+    float u[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float xi = x.get(i);
+        float c = fminf(fmaxf(fmaf(xi, inv, MAGIC), MAGIC - 8.f), MAGIC + 7.f);
+        if (sizeof(T) == 4 && byte) {
+            const float n = fabsf(c - MAGIC), a = fabsf(xi), sg = xi < 0.f ? -1.f : 1.f;
+            if (a < (n - 0.5f) * s) c -= sg;
+            else if (a >= (n + 0.5f) * s) c = fminf(fmaxf(c + sg, MAGIC - 8.f), MAGIC + 7.f);
+        }
+        u[i] = c;
+    }
+    if (kept) {
+        uint32_t w = __float_as_uint(u[7]);
+#pragma unroll
+        for (int i = 6; i >= 0; --i) w = w * 16u + __float_as_uint(u[i]);
+        // every term but the nibbles: the bits of 1.5 * 2^23, times 16^i
+        w -= 0x4B400000u * 0x11111111u;
+        *reinterpret_cast<uint32_t *>(page + (int64_t)t * (D / 2) + 4 * j) = w;
+        if ((j & 3) == 0) page[((int64_t)(D / 2) << lg_page) + t * (D / PG_GROUP) + (j >> 2)] = (uint8_t)byte;
+    }
+    if (so && live) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) u[i] = (u[i] - MAGIC) * s;
+        Eight<T>::store(so, u);
+    }
+}
+
+// Rows -> pages.  Each thread holds eight channels of the key and the value
+// of ROWS rows, all loaded before the first is used.
+template <typename T, int D, int ROWS>
+__global__ void __launch_bounds__(RW_THREADS) tq_paged_write_kernel(const __grid_constant__ RowsArg A) {
+    constexpr int LANES = D / 8, STEP = RW_THREADS / LANES;   // rows a block takes at once
+    const int j = threadIdx.x % LANES, r0 = threadIdx.x / LANES;
+    const int64_t base = (int64_t)blockIdx.x * (STEP * ROWS);
+    const int64_t base_token = base / A.H;
+    const int base_head = (int)(base - base_token * A.H);
+    const T *k = static_cast<const T *>(A.k), *v = static_cast<const T *>(A.v);
+    T *ko = static_cast<T *>(A.ko), *vo = static_cast<T *>(A.vo);
+    Eight<T> xk[ROWS], xv[ROWS];
+    int64_t slot[ROWS];
+    int head[ROWS];
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        const int local = r0 + i * STEP;
+        slot[i] = -1;
+        head[i] = 0;
+        xk[i].zero();
+        xv[i].zero();
+        if (base + local < A.n_rows) {
+            const Place p = place_of(A, base_token, base_head, local);
+            slot[i] = A.slots[p.token];
+            head[i] = p.head;
+            if (k) xk[i].load(k + p.token * A.skt + p.head * A.skh + 8 * j);
+            if (v) xv[i].load(v + p.token * A.svt + p.head * A.svh + 8 * j);
+        }
+    }
+    unsigned bad_rows = 0;
+    bool bad_slot = false;
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        const int64_t row = base + r0 + i * STEP;
+        const bool live = row < A.n_rows, kept = slot[i] >= 0 && slot[i] < A.n_slots;
+        bad_slot |= slot[i] >= A.n_slots;
+        const int t = kept ? (int)(slot[i] & ((1 << A.lg_page) - 1)) : 0;
+        const int64_t at = kept ? ((slot[i] >> A.lg_page) * A.H + head[i]) * A.page_bytes : 0;
+        if (k) quantise_store<T, D>(xk[i], live, kept, A.kc + at, t, A.lg_page, j, ko ? ko + row * D + 8 * j : nullptr, bad_rows);
+        if (v) quantise_store<T, D>(xv[i], live, kept, A.vc + at, t, A.lg_page, j, vo ? vo + row * D + 8 * j : nullptr, bad_rows);
+    }
+    if (bad_rows) atomicAdd(A.status, (unsigned long long)bad_rows);
+    if (bad_slot) atomicOr(reinterpret_cast<unsigned int *>(A.status + 1), TQ_FLAG_INDEX);
+}
+
+// Pages -> rows (exact in every type).  A slot outside the cache gives a row
+// of zeros.
+template <typename T, int D, int ROWS>
+__global__ void __launch_bounds__(RW_THREADS) tq_paged_read_kernel(const __grid_constant__ RowsArg A) {
+    constexpr int LANES = D / 8, STEP = RW_THREADS / LANES;
+    const int j = threadIdx.x % LANES, r0 = threadIdx.x / LANES;
+    const int64_t base = (int64_t)blockIdx.x * (STEP * ROWS);
+    const int64_t base_token = base / A.H;
+    const int base_head = (int)(base - base_token * A.H);
+    T *out[2] = {static_cast<T *>(A.ko), static_cast<T *>(A.vo)};
+    uint32_t w[ROWS][2], sb[ROWS][2];
+    bool bad_slot = false;
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        const int local = r0 + i * STEP;
+        int64_t slot = -1;
+        Place p{0, 0};
+        if (base + local < A.n_rows) {
+            p = place_of(A, base_token, base_head, local);
+            slot = A.slots[p.token];
+        }
+        bad_slot |= slot >= A.n_slots;
+        const bool kept = slot >= 0 && slot < A.n_slots;
+        const int t = (int)(slot & ((1 << A.lg_page) - 1));
+        const int64_t at = ((slot >> A.lg_page) * A.H + p.head) * A.page_bytes;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint8_t *c = h ? A.vc : A.kc;
+            w[i][h] = 0x88888888u;
+            sb[i][h] = 0;
+            if (kept && out[h]) {
+                w[i][h] = __ldg(reinterpret_cast<const uint32_t *>(c + at + (int64_t)t * (D / 2)) + j);
+                sb[i][h] = __ldg(c + at + ((int64_t)(D / 2) << A.lg_page) + t * (D / PG_GROUP) + (j >> 2));
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        const int64_t row = base + r0 + i * STEP;
+        if (row >= A.n_rows) continue;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (!out[h]) continue;
+            const float s = scale_value(sb[i][h]);
+            float x[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = (float)((int)((w[i][h] >> (4 * e)) & 15u) - 8) * s;
+            Eight<T>::store(out[h] + row * D + 8 * j, x);
+        }
+    }
+    if (bad_slot) atomicOr(reinterpret_cast<unsigned int *>(A.status + 1), TQ_FLAG_INDEX);
+}
+
+template <typename T, int D>
+cudaError_t launch_rows(bool write, const RowsArg &A, int n_sms, cudaStream_t stream) {
+    constexpr int STEP = RW_THREADS / (D / 8);
+    // several rows a thread keep more loads in flight; few rows are spread
+    // over as many SMs as they reach
+    constexpr int MANY = sizeof(T) == 4 ? 2 : 4;
+    const bool many = A.n_rows >= (int64_t)STEP * MANY * n_sms * 2;
+    const int64_t blocks = (A.n_rows + (many ? STEP * MANY : STEP) - 1) / (many ? STEP * MANY : STEP);
+    if (write) {
+        if (many) tq_paged_write_kernel<T, D, MANY><<<(unsigned)blocks, RW_THREADS, 0, stream>>>(A);
+        else tq_paged_write_kernel<T, D, 1><<<(unsigned)blocks, RW_THREADS, 0, stream>>>(A);
+    } else {
+        if (many) tq_paged_read_kernel<T, D, MANY><<<(unsigned)blocks, RW_THREADS, 0, stream>>>(A);
+        else tq_paged_read_kernel<T, D, 1><<<(unsigned)blocks, RW_THREADS, 0, stream>>>(A);
+    }
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_rows_d(int d, bool write, const RowsArg &A, int n_sms, cudaStream_t stream) {
+    if (d == 64) return launch_rows<T, 64>(write, A, n_sms, stream);
+    if (d == 128) return launch_rows<T, 128>(write, A, n_sms, stream);
+    return launch_rows<T, 256>(write, A, n_sms, stream);
+}
+
+bool dtype_ok(tq_dtype t) { return t == TQ_F32 || t == TQ_F16 || t == TQ_BF16; }
+
+bool misaligned(const void *p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
+
+int log2_of(int x) {
+    int l = 0;
+    while ((1 << l) < x) ++l;
+    return l;
+}
+
+tq_status check_paged_device(const tq_paged *c) {
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess) return TQ_ERR_CUDA;
+    return dev == c->device ? TQ_OK : TQ_ERR_DEVICE;
+}
+
+int64_t page_bytes_of(const tq_paged *c) { return (int64_t)c->page * (c->d / 2 + c->d / PG_GROUP); }
+
+tq_status check_pages(const tq_paged *c, const tq_pages *p, bool need_k, bool need_v) {
+    if (!c || !p) return TQ_ERR_NULL;
+    if ((need_k && !p->k) || (need_v && !p->v)) return TQ_ERR_NULL;
+    if (p->n_kv_heads <= 0 || p->n_pages <= 0) return TQ_ERR_EMPTY;
+    if (p->n_kv_heads > TQ_MAX_HEADS || p->n_pages > INT_MAX) return TQ_ERR_LIMIT;
+    if ((need_k && misaligned(p->k, 16)) || (need_v && misaligned(p->v, 16))) return TQ_ERR_ALIGN;
+    return TQ_OK;
+}
+
+tq_status run_rows(tq_paged *ctx, bool write, const tq_pages *pages, RowsArg &A, const int64_t *slots, int64_t n_tokens,
+                   tq_dtype dtype, void *stream) {
+    if (!dtype_ok(dtype) || n_tokens < 0) return TQ_ERR_DIM_MISMATCH;
+    tq_status st = check_paged_device(ctx);
+    if (st != TQ_OK) return st;
+    if (n_tokens == 0) return TQ_OK;
+    if (!slots) return TQ_ERR_NULL;
+    if (misaligned(slots, 8)) return TQ_ERR_ALIGN;
+    if (n_tokens > INT_MAX || n_tokens * pages->n_kv_heads > (int64_t)INT_MAX * 4) return TQ_ERR_LIMIT;
+    A.kc = static_cast<uint8_t *>(pages->k);
+    A.vc = static_cast<uint8_t *>(pages->v);
+    A.slots = slots;
+    A.H = pages->n_kv_heads;
+    A.inv_H = ((1ull << 32) + A.H - 1) / A.H;
+    A.lg_page = log2_of(ctx->page);
+    A.n_rows = n_tokens * A.H;
+    A.n_slots = pages->n_pages * ctx->page;
+    A.page_bytes = page_bytes_of(ctx);
+    A.status = ctx->d_status;
+    const int sms = tq_device_sms(ctx->device);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (dtype == TQ_F32) return tq_check_cuda(launch_rows_d<float>(ctx->d, write, A, sms, s));
+    if (dtype == TQ_F16) return tq_check_cuda(launch_rows_d<__half>(ctx->d, write, A, sms, s));
+    return tq_check_cuda(launch_rows_d<__nv_bfloat16>(ctx->d, write, A, sms, s));
+}
+
+}  // namespace
+
+extern "C" {
+
+tq_status tq_paged_create(int head_dim, int page_size, tq_paged **out) {
+    if (!out) return TQ_ERR_NULL;
+    *out = nullptr;
+    if (head_dim == 0) return TQ_ERR_ZERO_DIM;
+    if (head_dim != 64 && head_dim != 128 && head_dim != 256) return TQ_ERR_DIM;
+    if (page_size < 16 || page_size > 256 || (page_size & (page_size - 1))) return TQ_ERR_DIM_MISMATCH;
+    int dev = -1, major = 0, minor = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return TQ_ERR_CUDA;
+    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
+        return TQ_ERR_CUDA;
+    if (major != 10 || minor != 0) return TQ_ERR_DEVICE;
+    unsigned long long *status = nullptr;
+    tq_status st = tq_check_cuda(cudaMalloc(&status, 2 * sizeof(unsigned long long)));
+    if (st == TQ_OK) st = tq_check_cuda(cudaMemset(status, 0, 2 * sizeof(unsigned long long)));
+    if (st == TQ_OK) st = tq_check_cuda(cudaDeviceSynchronize());
+    tq_paged *c = st == TQ_OK ? new (std::nothrow) tq_paged{head_dim, page_size, dev, status} : nullptr;
+    if (!c) {
+        cudaFree(status);
+        return st == TQ_OK ? TQ_ERR_LIMIT : st;
+    }
+    *out = c;
+    return TQ_OK;
+}
+
+void tq_paged_destroy(tq_paged *ctx) {
+    if (!ctx) return;
+    int dev = -1;
+    cudaGetDevice(&dev);
+    if (dev != ctx->device) cudaSetDevice(ctx->device);
+    cudaDeviceSynchronize();
+    cudaFree(ctx->d_status);
+    if (dev >= 0 && dev != ctx->device) cudaSetDevice(dev);
+    delete ctx;
+}
+
+int64_t tq_paged_page_bytes(const tq_paged *ctx) { return ctx ? page_bytes_of(ctx) : 0; }
+
+tq_status tq_paged_write(tq_paged *ctx, const void *k, const void *v, tq_dtype dtype, int64_t n_tokens,
+                         int64_t stride_kt, int64_t stride_kh, int64_t stride_vt, int64_t stride_vh,
+                         const int64_t *slots, const tq_pages *pages, void *k_stored, void *v_stored, void *stream) {
+    if (!ctx || !pages) return TQ_ERR_NULL;
+    if (n_tokens != 0 && !k && !v) return TQ_ERR_NULL;
+    if ((k_stored && !k) || (v_stored && !v)) return TQ_ERR_NULL;
+    tq_status st = check_pages(ctx, pages, k != nullptr, v != nullptr);
+    if (st != TQ_OK) return st;
+    if (!dtype_ok(dtype)) return TQ_ERR_DIM_MISMATCH;
+    const int64_t es = dtype == TQ_F32 ? 4 : 2;
+    if (misaligned(k, 16) || misaligned(v, 16) || misaligned(k_stored, 16) || misaligned(v_stored, 16) ||
+        (k && (stride_kt * es % 16 || stride_kh * es % 16)) || (v && (stride_vt * es % 16 || stride_vh * es % 16)))
+        return TQ_ERR_ALIGN;
+    RowsArg A = {};
+    A.k = k;
+    A.v = v;
+    A.ko = k_stored;
+    A.vo = v_stored;
+    A.skt = stride_kt;
+    A.skh = stride_kh;
+    A.svt = stride_vt;
+    A.svh = stride_vh;
+    return run_rows(ctx, true, pages, A, slots, n_tokens, dtype, stream);
+}
+
+tq_status tq_paged_read(tq_paged *ctx, const tq_pages *pages, const int64_t *slots, int64_t n_tokens, void *k_out,
+                        void *v_out, tq_dtype dtype, void *stream) {
+    if (!ctx || !pages) return TQ_ERR_NULL;
+    if (n_tokens != 0 && !k_out && !v_out) return TQ_ERR_NULL;
+    tq_status st = check_pages(ctx, pages, k_out != nullptr, v_out != nullptr);
+    if (st != TQ_OK) return st;
+    if (misaligned(k_out, 16) || misaligned(v_out, 16)) return TQ_ERR_ALIGN;
+    RowsArg A = {};
+    A.ko = k_out;
+    A.vo = v_out;
+    return run_rows(ctx, false, pages, A, slots, n_tokens, dtype, stream);
+}
+
+}  // extern "C"
+
+// The checks of an attention call, and its description for the kernels.
+static tq_status describe(const tq_paged *ctx, const tq_pages *pages, const void *q, tq_dtype dtype, int64_t total_q,
+                          int n_q_heads, int64_t stride_qt, int64_t stride_qh, const int32_t *page_table,
+                          int64_t table_stride, int64_t max_pages, const int32_t *seq_lens, const int32_t *q_starts,
+                          int batch, int max_q_len, int window, int sinks, float scale, void *out, int64_t stride_ot,
+                          int64_t stride_oh, PagedAttn &P) {
+    tq_status st = check_pages(ctx, pages, true, true);
+    if (st != TQ_OK) return st;
+    if (dtype != TQ_F16 && dtype != TQ_BF16) return TQ_ERR_DIM_MISMATCH;
+    if (batch <= 0 || n_q_heads <= 0 || max_q_len <= 0) return TQ_ERR_EMPTY;
+    if (n_q_heads % pages->n_kv_heads || total_q < 0 || (!q_starts && total_q != batch)) return TQ_ERR_DIM_MISMATCH;
+    if (max_pages < 0 || table_stride < max_pages || window < 0 || sinks < 0 || !std::isfinite(scale) || scale < 0.f)
+        return TQ_ERR_DIM_MISMATCH;
+    if (n_q_heads > TQ_MAX_HEADS || batch > TQ_MAX_PAGED_SEQS || total_q * n_q_heads > INT_MAX / 2 ||
+        max_pages * ctx->page > INT_MAX / 2 || window > INT_MAX / 2)
+        return TQ_ERR_LIMIT;
+    if (total_q > 0) {
+        if (!q || !out || !seq_lens || (!page_table && max_pages > 0)) return TQ_ERR_NULL;
+        if (misaligned(q, 16) || misaligned(out, 16) || stride_qt % 8 || stride_qh % 8 || stride_ot % 8 || stride_oh % 8 ||
+            misaligned(page_table, 4) || misaligned(seq_lens, 4) || misaligned(q_starts, 4))
+            return TQ_ERR_ALIGN;
+    }
+    P = PagedAttn{};
+    P.kc = static_cast<const uint8_t *>(pages->k);
+    P.vc = static_cast<const uint8_t *>(pages->v);
+    P.n_pages = pages->n_pages;
+    P.page_bytes = page_bytes_of(ctx);
+    P.lg_page = log2_of(ctx->page);
+    P.Hkv = pages->n_kv_heads;
+    P.G = n_q_heads / pages->n_kv_heads;
+    P.batch = batch;
+    P.total_q = (int)total_q;
+    P.q = q;
+    P.out = out;
+    P.sqt = stride_qt;
+    P.sqh = stride_qh;
+    P.sot = stride_ot;
+    P.soh = stride_oh;
+    P.bf16 = dtype == TQ_BF16;
+    P.table = page_table;
+    P.table_stride = table_stride;
+    P.max_tokens = (int)(max_pages * ctx->page);
+    P.lens = seq_lens;
+    P.starts = q_starts;
+    P.window = window;
+    P.sinks = sinks;
+    P.scale_log2 = (scale > 0.f ? scale : 1.f / std::sqrt((float)ctx->d)) * 1.4426950408889634f;
+    P.status = ctx->d_status;
+    return TQ_OK;
+}
+
+extern "C" {
+
+size_t tq_paged_workspace_bytes(const tq_paged *ctx, int n_q_heads, int n_kv_heads, int batch, int64_t max_pages,
+                                int max_q_len) {
+    if (!ctx || n_q_heads <= 0 || n_kv_heads <= 0 || n_q_heads % n_kv_heads || batch <= 0 || max_pages < 0 ||
+        max_q_len <= 0 || max_pages * ctx->page > INT_MAX / 2)
+        return 0;
+    PagedAttn P = {};
+    P.Hkv = n_kv_heads;
+    P.G = n_q_heads / n_kv_heads;
+    P.batch = batch;
+    P.max_tokens = (int)(max_pages * ctx->page);
+    size_t need = 0;
+    tq_launch_paged_attention(ctx, P, max_q_len, tq_device_sms(ctx->device), nullptr, &need);
+    return need;
+}
+
+tq_status tq_paged_attention(tq_paged *ctx, const tq_pages *pages, const void *q, tq_dtype dtype, int64_t total_q,
+                             int n_q_heads, int64_t stride_qt, int64_t stride_qh, const int32_t *page_table,
+                             int64_t table_stride, int64_t max_pages, const int32_t *seq_lens, const int32_t *q_starts,
+                             int batch, int max_q_len, int window, int sinks, float scale, void *out,
+                             int64_t stride_ot, int64_t stride_oh, void *workspace, size_t ws_bytes, void *stream) {
+    if (!ctx || !pages) return TQ_ERR_NULL;
+    PagedAttn P;
+    tq_status st = describe(ctx, pages, q, dtype, total_q, n_q_heads, stride_qt, stride_qh, page_table, table_stride,
+                            max_pages, seq_lens, q_starts, batch, max_q_len, window, sinks, scale, out, stride_ot,
+                            stride_oh, P);
+    if (st != TQ_OK) return st;
+    if ((st = check_paged_device(ctx)) != TQ_OK) return st;
+    if (total_q == 0) return TQ_OK;
+    const size_t need = tq_paged_workspace_bytes(ctx, n_q_heads, pages->n_kv_heads, batch, max_pages, max_q_len);
+    if (!workspace || ws_bytes < need) return TQ_ERR_WORKSPACE;
+    if (misaligned(workspace, 16)) return TQ_ERR_ALIGN;
+    P.part = static_cast<float *>(workspace);
+    return tq_launch_paged_attention(ctx, P, max_q_len, tq_device_sms(ctx->device), static_cast<cudaStream_t>(stream),
+                                     nullptr);
+}
+
+tq_status tq_paged_get_status(tq_paged *ctx, void *stream, uint64_t *nonfinite_rows, uint32_t *error_flags) {
+    if (!ctx) return TQ_ERR_NULL;
+    unsigned long long h[2] = {0, 0};
+    tq_status st = tq_check_cuda(cudaStreamSynchronize(static_cast<cudaStream_t>(stream)));
+    if (st == TQ_OK) st = tq_check_cuda(cudaMemcpy(h, ctx->d_status, sizeof(h), cudaMemcpyDeviceToHost));
+    if (st != TQ_OK) return st;
+    if (nonfinite_rows) *nonfinite_rows = h[0];
+    if (error_flags) *error_flags = (uint32_t)h[1];
+    return TQ_OK;
+}
+
+tq_status tq_paged_reset_status(tq_paged *ctx, void *stream) {
+    if (!ctx) return TQ_ERR_NULL;
+    return tq_check_cuda(
+        cudaMemsetAsync(ctx->d_status, 0, 2 * sizeof(unsigned long long), static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -1,0 +1,624 @@
+// tq_paged_attend.cu -- attention over the paged 4-bit cache for few queries
+// a sequence: decode steps, drafted tokens.
+//
+//   s_t = q . k_t / sqrt(d),  o = sum_t softmax(s)_t v_t  over the visible t:
+//   t <= p, and, under a window W with S sinks, t > p - W or t < S,
+// where p is the query's position and k_t, v_t are what the codes stand for.
+//
+// What bounds it: a token of one kv head is 17 d / 16 bytes (136 at d = 128)
+// and is used by few rows (queries times query heads of the group), so the
+// floor is the time to read the visible tokens.  At HBM rate an SM has about
+// 94 cycles for 16 tokens, that is some 370 warp instructions to turn 4096
+// codes into operands, multiply and take the softmax.  Hence:
+//   * codes go from shared memory into registers as the fragments of
+//     mma.m16n8k16 (tokens or channels as the 16 rows, queries as the 8
+//     columns) and are widened there: no operand is written back to shared
+//     memory, which tcgen05 would need (64 KB for 128 tokens, more than the
+//     shared-memory bandwidth allows at this rate);
+//   * a lane takes consecutive code words, and the contraction runs over the
+//     channels in the order that this gives; the query's fragments are built
+//     in the same order;
+//   * code pairs are spliced into the mantissa of 1024 + c or 64 + c and
+//     brought to c s by one or two packed operations, exactly;
+//   * each warp streams its own tiles through its own ring of stages, filled
+//     by bulk copies of whole (parts of) pages; warps meet only where an
+//     item ends.
+// The probabilities are rounded to binary16 (error 2^-12 of each weight,
+// half a rounding step of a binary16 output); queries are taken to binary16
+// after a power-of-two scaling by their largest channel (bfloat16; exact
+// unless a channel is below 2^-28 of the largest), keys and values are exact
+// in binary16, and scores, maxima, sums and outputs are float32.
+#include <algorithm>
+
+#include "tq_paged.cuh"
+
+namespace {
+
+using namespace tqpaged;
+
+constexpr int NW = 4;                  // warps of a CTA
+constexpr int THREADS = 32 * NW;
+constexpr float RAISE = 8.f;           // the running maximum is raised when a score passes it by 2^8
+constexpr float BIAS = 6.f;            // weights are 2^(s - m + 6): at most 2^14, and exact to 2^-20
+
+template <int D>
+struct Cfg {
+    static constexpr int TT = D == 256 ? 32 : 64;              // tokens of a tile
+    static constexpr int NST = D == 64 ? 3 : 2;                // stages of a warp
+    static constexpr int CTAS = D == 64 ? 4 : 3;               // CTAs of an SM
+    static constexpr int CODES = TT * D / 2, SCALES = TT * D / 32;
+    static constexpr int STAGE = 2 * (CODES + SCALES);         // K codes, V codes, K scales, V scales
+    static constexpr int SMEM = NW * NST * STAGE;
+};
+
+__device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<uint32_t *>(&h); }
+__device__ __forceinline__ __half2 u2h(uint32_t u) { return *reinterpret_cast<__half2 *>(&u); }
+
+__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t bits) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "r"(mask), "r"(bits));   // (w & mask) | bits
+    return r;
+}
+
+// Pairs of codes in nibbles 0..3 of both halves of w, times the scales of
+// the two halves: p[i] = ((nibble i of the low half) - 8) s.x, the same of
+// the high half and s.y.  m72s = -72 s (exact: 9 times four bits).
+__device__ __forceinline__ void widen(uint32_t w, __half2 s, __half2 m72s, uint32_t (&p)[4]) {
+    const __half2 m1032 = __half2half2(__ushort_as_half((unsigned short)0xE408));   // -1032
+    const uint32_t w8 = w >> 8;
+    p[0] = h2u(__hmul2(__hadd2(u2h(and_or(w, 0x000F000Fu, 0x64006400u)), m1032), s));
+    p[1] = h2u(__hfma2(u2h(and_or(w, 0x00F000F0u, 0x54005400u)), s, m72s));
+    p[2] = h2u(__hmul2(__hadd2(u2h(and_or(w8, 0x000F000Fu, 0x64006400u)), m1032), s));
+    p[3] = h2u(__hfma2(u2h(and_or(w8, 0x00F000F0u, 0x54005400u)), s, m72s));
+}
+
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// WORDS consecutive 32-bit words of shared memory.
+template <int WORDS>
+__device__ __forceinline__ void load_words(const uint8_t *p, uint32_t (&w)[WORDS]) {
+    if constexpr (WORDS == 1) {
+        w[0] = *reinterpret_cast<const uint32_t *>(p);
+    } else if constexpr (WORDS == 2) {
+        const uint2 x = *reinterpret_cast<const uint2 *>(p);
+        w[0] = x.x, w[1] = x.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < WORDS; i += 4) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(p + 4 * i);
+            w[i] = x.x, w[i + 1] = x.y, w[i + 2] = x.z, w[i + 3] = x.w;
+        }
+    }
+}
+
+// The query fragments of an item's rows.  Lane (g, t) holds row 8 nt + g,
+// channels [t D/4, (t + 1) D/4), in pairs (e, e + 4) of each eight: the order
+// in which widen() gives the codes.  `mul[nt][c]` is what turns the product
+// of column 2 t + c into a score in units of log2.
+template <int D, int NT>
+__device__ __forceinline__ void load_queries(const PagedAttn &P, const Seq &s, int h, int row0, int row1, int lane,
+                                             uint32_t (&q)[NT][D / 8], float (&mul)[NT][2]) {
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const int row = row0 + 8 * nt + g;
+        uint4 w[D / 32];
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) w[i] = make_uint4(0, 0, 0, 0);
+        if (row < row1) {
+            const int tok = row / P.G, hg = row - tok * P.G;
+            const int64_t at = (int64_t)(s.q0 + tok) * P.sqt + (int64_t)(h * P.G + hg) * P.sqh + t * (D / 4);
+            const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(P.q) + at);
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) w[i] = __ldg(src + i);
+        }
+        float back = 1.f;
+        if (P.bf16) {
+            uint32_t m = 0;
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i)
+                m = __vmaxu2(m, __vmaxu2(__vmaxu2(w[i].x & 0x7FFF7FFFu, w[i].y & 0x7FFF7FFFu),
+                                         __vmaxu2(w[i].z & 0x7FFF7FFFu, w[i].w & 0x7FFF7FFFu)));
+            m = max(m >> 16, m & 0xFFFFu);
+            m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+            m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+            // largest channel to [2^14, 2^15); the factor stays a normal float
+            const int e = min(max((int)(m >> 7), 15), 254);
+            const float up = __uint_as_float((uint32_t)(268 - e) << 23);   // 2^(141 - e)
+            back = __uint_as_float((uint32_t)(e - 14) << 23);              // 2^(e - 141)
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    x[j] = h2u(__floats2half2_rn(__uint_as_float(x[j] << 16) * up, __uint_as_float(x[j] & 0xFFFF0000u) * up));
+                w[i] = make_uint4(x[0], x[1], x[2], x[3]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {   // elements 0..7 of a word: pairs (0,4) (1,5) (2,6) (3,7)
+            q[nt][4 * i + 0] = __byte_perm(w[i].x, w[i].z, 0x5410);
+            q[nt][4 * i + 1] = __byte_perm(w[i].x, w[i].z, 0x7632);
+            q[nt][4 * i + 2] = __byte_perm(w[i].y, w[i].w, 0x5410);
+            q[nt][4 * i + 3] = __byte_perm(w[i].y, w[i].w, 0x7632);
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c) mul[nt][c] = __shfl_sync(0xffffffffu, back, (2 * t + c) * 4) * P.scale_log2;
+    }
+}
+
+__device__ __forceinline__ void store_out4(const PagedAttn &P, int64_t at, float4 v) {
+    uint2 o;
+    if (P.bf16) {
+        const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+        o = make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+    } else {
+        o = make_uint2(h2u(__floats2half2_rn(v.x, v.y)), h2u(__floats2half2_rn(v.z, v.w)));
+    }
+    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(P.out) + at) = o;
+}
+
+// Element offset of row `row` of (sequence, kv head) in the output.
+__device__ __forceinline__ int64_t out_at(const PagedAttn &P, const Seq &s, int h, int row) {
+    const int tok = row / P.G, hg = row - tok * P.G;
+    return (int64_t)(s.q0 + tok) * P.sot + (int64_t)(h * P.G + hg) * P.soh;
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(THREADS, Cfg<D>::CTAS) tq_paged_decode_kernel(const __grid_constant__ PagedAttn P) {
+    using C = Cfg<D>;
+    constexpr int TT = C::TT, NST = C::NST, R = 8 * NT, KW = D / 32, VW = D / 64, SUB = TT / 16;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ __align__(8) uint64_t bars[NW][NST];
+    __shared__ float s_m[NW][R], s_l[NW][R];
+    __shared__ Share s_share;
+    __shared__ long long s_sum[NW];
+    __shared__ int s_abort;
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    if (tid == 0) {
+        s_abort = tqdev::status_aborted(P.status) ? 1 : 0;
+        for (int w = 0; w < NW; ++w)
+            for (int i = 0; i < NST; ++i) tqdev::mbar_init(&bars[w][i], 1);
+        tqdev::fence_barrier_init();
+    }
+    tqdev::grid_dep_trigger();
+    const Share sh = find_share<R, TT, THREADS>(P, &s_share, s_sum);
+    if (tid == 0) P.rec[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    if (s_abort || sh.lo >= sh.hi) return;
+
+    uint8_t *ring = smem + warp * (NST * C::STAGE);
+    uint64_t *bar = bars[warp];
+    int used = 0, filled = 0;         // tiles of this warp consumed and requested, over all items
+    uint32_t valid_pages = 0;         // four bits a stage: which parts of the tile were copied
+    bool failed = false;
+
+    // the place of the first tile: sequence, kv head, first row, tile
+    int b = sh.b;
+    bool bad = false;
+    Seq s = load_seq(P, b, bad);
+    int h, row0 = 0;
+    long long into = sh.into;
+    {
+        const long long per_head = head_tiles<R, TT>(P, s);
+        h = (int)(into / per_head);
+        into -= h * per_head;
+        for (;; row0 += R) {
+            const int n = chunk_tiles<TT>(P, s, row0, min(s.n * P.G, row0 + R)).n;
+            if (into < n) break;
+            into -= n;
+        }
+    }
+    long long at = sh.lo;             // tiles done
+
+    while (at < sh.hi) {
+        const int row1 = min(s.n * P.G, row0 + R);
+        const Tiles tl = chunk_tiles<TT>(P, s, row0, row1);
+        const int i0 = (int)into, i1 = (int)min((long long)tl.n, into + (sh.hi - at));
+        const int *table = P.table + (int64_t)b * P.table_stride;
+        const int lg_part = min(P.lg_page, TT == 64 ? 6 : 5), parts = TT >> lg_part;
+
+        // The page number of this lane's part of a tile, fetched one tile ahead.
+        auto fetch = [&](int i) -> int {
+            const int tok = tile_token(tl, i, TT) + (lane << lg_part);
+            return (i < i1 && lane < parts && tok < s.len) ? __ldg(table + (tok >> P.lg_page)) : -1;
+        };
+        int next_page = fetch(i0 + warp);
+        auto request = [&](int i) {
+            const int st = filled % NST;
+            const int tok = tile_token(tl, i, TT) + (lane << lg_part);
+            const int page = next_page;
+            next_page = fetch(i + NW);
+            const bool live = lane < parts && tok < s.len;
+            const bool ok = live && page >= 0 && page < P.n_pages;
+            if (live && !ok) atomicOr(reinterpret_cast<unsigned int *>(P.status + 1), TQ_FLAG_INDEX);
+            const uint32_t got = __ballot_sync(0xffffffffu, ok);
+            valid_pages = (valid_pages & ~(15u << (4 * st))) | ((got & 15u) << (4 * st));
+            const uint32_t codes = (uint32_t)(D / 2) << lg_part, scales = (uint32_t)(D / 32) << lg_part;
+            if (lane == 0) tqdev::mbar_expect_tx(&bar[st], (uint32_t)__popc(got) * 2u * (codes + scales));
+            __syncwarp();
+            if (ok) {
+                uint8_t *dst = ring + st * C::STAGE;
+                const int64_t src = ((int64_t)page * P.Hkv + h) * P.page_bytes;
+                const int in = tok & ((1 << P.lg_page) - 1);
+                const int64_t c0 = src + (int64_t)in * (D / 2);
+                const int64_t s0 = src + ((int64_t)(D / 2) << P.lg_page) + (int64_t)in * (D / 32);
+                tqdev::bulk_load(dst + lane * codes, P.kc + c0, codes, &bar[st]);
+                tqdev::bulk_load(dst + C::CODES + lane * codes, P.vc + c0, codes, &bar[st]);
+                tqdev::bulk_load(dst + 2 * C::CODES + lane * scales, P.kc + s0, scales, &bar[st]);
+                tqdev::bulk_load(dst + 2 * C::CODES + C::SCALES + lane * scales, P.vc + s0, scales, &bar[st]);
+            }
+            ++filled;
+        };
+
+        int ahead = i0 + warp;
+        for (int k = 0; k < NST; ++k, ahead += NW)
+            if (ahead < i1 && !failed) request(ahead);
+
+        uint32_t q[NT][D / 8];
+        float mul[NT][2], m_run[NT][2], l_run[NT][2], o[NT][D / 16][4];
+        int pos[NT][2];               // position of the query of column 2 t + c
+        load_queries<D, NT>(P, s, h, row0, row1, lane, q, mul);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                m_run[nt][c] = -INFINITY;
+                l_run[nt][c] = 0.f;
+                pos[nt][c] = s.len - s.n + (row0 + 8 * nt + 2 * t + c) / P.G;
+            }
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[nt][j][e] = 0.f;
+        }
+
+        for (int i = i0 + warp; i < i1 && !failed; i += NW) {
+            const int st = used % NST;
+            if (!__all_sync(0xffffffffu, tqdev::mbar_wait_bounded(&bar[st], (uint32_t)(used / NST) & 1u))) {
+                failed = true;
+                break;
+            }
+            const uint8_t *kc = ring + st * C::STAGE, *vc = kc + C::CODES, *ks = vc + C::CODES, *vs = ks + C::SCALES;
+            const int T0 = tile_token(tl, i, TT);
+            const uint32_t got = valid_pages >> (4 * st);
+            const bool whole = T0 + TT - 1 <= tl.p_lo && (P.window <= 0 || T0 > tl.p_hi - P.window || T0 + TT <= P.sinks) &&
+                               (got & ((1u << parts) - 1u)) == (1u << parts) - 1u;
+
+            // scores: 16 tokens a step; rows g and g + 8 of the fragment are
+            // the tokens (g / 2) + 4 (g % 2) and that + 8, so that the
+            // transposed weights come out in the order of the value loads
+            float sc[NT][SUB][4];
+            const int tok0 = (g >> 1) + 4 * (g & 1);
+#pragma unroll
+            for (int u = 0; u < SUB; ++u) {
+                uint32_t w0[KW], w1[KW];
+                const int ra = 16 * u + tok0, rb = ra + 8;
+                load_words<KW>(kc + ra * (D / 2) + t * (D / 8), w0);
+                load_words<KW>(kc + rb * (D / 2) + t * (D / 8), w1);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sc[nt][u][e] = 0.f;
+#pragma unroll
+                for (int x = 0; x < KW; x += (D == 256 ? 4 : KW)) {   // the words of one group
+                    const int grp = D == 64 ? t >> 1 : D == 128 ? t : 2 * t + x / 4;
+                    const __half2 s0 = u2h(ks[ra * (D / 32) + grp] * 0x00800080u);
+                    const __half2 s1 = u2h(ks[rb * (D / 32) + grp] * 0x00800080u);
+                    const __half2 m72 = __half2half2(__ushort_as_half((unsigned short)0xD480));   // -72
+                    const __half2 b0 = __hmul2(s0, m72), b1 = __hmul2(s1, m72);
+#pragma unroll
+                    for (int y = x; y < x + (D == 256 ? 4 : KW); ++y) {
+                        uint32_t a[4], c[4];
+                        widen(w0[y], s0, b0, a);
+                        widen(w1[y], s1, b1, c);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            mma(sc[nt][u], a[0], c[0], a[1], c[1], q[nt][4 * y], q[nt][4 * y + 1]);
+                            mma(sc[nt][u], a[2], c[2], a[3], c[3], q[nt][4 * y + 2], q[nt][4 * y + 3]);
+                        }
+                    }
+                }
+            }
+            if (!whole) {
+#pragma unroll
+                for (int u = 0; u < SUB; ++u) {
+                    const bool have = (got >> ((16 * u) >> lg_part)) & 1u;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int tok = T0 + 16 * u + tok0 + (e >= 2 ? 8 : 0);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            const int p = pos[nt][e & 1];
+                            const bool see = have && tok <= p && (P.window <= 0 || tok > p - P.window || tok < P.sinks);
+                            if (!see) sc[nt][u][e] = -INFINITY;
+                        }
+                    }
+                }
+            }
+            // softmax: raise the maximum only when some score passes it by RAISE
+            float mx[NT][2];
+            bool raise = false;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float m = fmaxf(sc[nt][0][c], sc[nt][0][c + 2]);
+#pragma unroll
+                    for (int u = 1; u < SUB; ++u) m = fmaxf(m, fmaxf(sc[nt][u][c], sc[nt][u][c + 2]));
+                    mx[nt][c] = m * mul[nt][c];
+                    raise |= mx[nt][c] > m_run[nt][c] + RAISE;
+                }
+            if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        float m = mx[nt][c];
+                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+                        m = fmaxf(m, m_run[nt][c]);
+                        const float f = m_run[nt][c] == -INFINITY ? 0.f : exp2_fast(m_run[nt][c] - m);
+                        m_run[nt][c] = m;
+                        l_run[nt][c] *= f;
+#pragma unroll
+                        for (int j = 0; j < D / 16; ++j) {
+                            o[nt][j][c] *= f;
+                            o[nt][j][c + 2] *= f;
+                        }
+                    }
+            }
+            uint32_t pw[NT][SUB][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const float r0 = m_run[nt][0] == -INFINITY ? 0.f : m_run[nt][0] - BIAS;
+                const float r1 = m_run[nt][1] == -INFINITY ? 0.f : m_run[nt][1] - BIAS;
+#pragma unroll
+                for (int u = 0; u < SUB; ++u) {
+                    const float p0 = exp2_fast(fmaf(sc[nt][u][0], mul[nt][0], -r0)), p1 = exp2_fast(fmaf(sc[nt][u][1], mul[nt][1], -r1));
+                    const float p2 = exp2_fast(fmaf(sc[nt][u][2], mul[nt][0], -r0)), p3 = exp2_fast(fmaf(sc[nt][u][3], mul[nt][1], -r1));
+                    l_run[nt][0] += p0 + p2;
+                    l_run[nt][1] += p1 + p3;
+                    pw[nt][u][0] = transpose8(h2u(__floats2half2_rn(p0, p1)));
+                    pw[nt][u][1] = transpose8(h2u(__floats2half2_rn(p2, p3)));
+                }
+            }
+            // values: lane (g, t) takes channels [g D/8, (g + 1) D/8) of the
+            // tokens t, t + 4, t + 8, t + 12 of each sixteen
+#pragma unroll
+            for (int u = 0; u < SUB; ++u) {
+                uint32_t w[4][VW], sv[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int r = 16 * u + t + 4 * k;
+                    load_words<VW>(vc + r * (D / 2) + g * (D / 16), w[k]);
+                    sv[k] = vs[r * (D / 32) + (g * (D / 8)) / 32];
+                    // rows that hold no token of this sequence may hold anything
+                    if (!whole && (T0 + r >= s.len || !((got >> ((16 * u) >> lg_part)) & 1u))) sv[k] = 0;
+                }
+                const __half2 m72 = __half2half2(__ushort_as_half((unsigned short)0xD480));
+                const __half2 s0 = u2h(sv[0] * 0x80u + sv[1] * 0x800000u), s1 = u2h(sv[2] * 0x80u + sv[3] * 0x800000u);
+                const __half2 b0 = __hmul2(s0, m72), b1 = __hmul2(s1, m72);
+#pragma unroll
+                for (int y = 0; y < VW; ++y) {
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const uint32_t sel = half ? 0x7632u : 0x5410u;
+                        uint32_t a[4], c[4];
+                        widen(__byte_perm(w[0][y], w[1][y], sel), s0, b0, a);
+                        widen(__byte_perm(w[2][y], w[3][y], sel), s1, b1, c);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            mma(o[nt][4 * y + 2 * half], a[0], a[1], c[0], c[1], pw[nt][u][0], pw[nt][u][1]);
+                            mma(o[nt][4 * y + 2 * half + 1], a[2], a[3], c[2], c[3], pw[nt][u][0], pw[nt][u][1]);
+                        }
+                    }
+                }
+            }
+            ++used;
+            __syncwarp();
+            if (ahead < i1) {
+                request(ahead);
+                ahead += NW;
+            }
+        }
+
+        // the warps' parts of this item, joined through shared memory
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                float l = l_run[nt][c];
+                l += __shfl_xor_sync(0xffffffffu, l, 4);
+                l += __shfl_xor_sync(0xffffffffu, l, 8);
+                l += __shfl_xor_sync(0xffffffffu, l, 16);
+                if (g == 0) {
+                    s_m[warp][8 * nt + 2 * t + c] = m_run[nt][c];
+                    s_l[warp][8 * nt + 2 * t + c] = l;
+                }
+            }
+        __syncthreads();
+        float *mine = reinterpret_cast<float *>(ring);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int r = 8 * nt + 2 * t + c;
+                float m = s_m[0][r];
+#pragma unroll
+                for (int w = 1; w < NW; ++w) m = fmaxf(m, s_m[w][r]);
+                const float f = m_run[nt][c] == -INFINITY ? 0.f : exp2_fast(m_run[nt][c] - m);
+                if (!failed) {
+#pragma unroll
+                    for (int j = 0; j < D / 16; ++j)
+                        *reinterpret_cast<float2 *>(mine + r * D + g * (D / 8) + 8 * (j >> 2) + 2 * (j & 3)) =
+                            make_float2(o[nt][j][c] * f, o[nt][j][c + 2] * f);
+                }
+            }
+        __syncthreads();
+        const bool begins = i0 == 0, ends = i1 == tl.n;
+        float *part = P.part + ((int64_t)blockIdx.x * 2 + (begins ? 1 : 0)) * (R * (D + 2));
+        for (int x = tid; x < R * D / 4; x += THREADS) {
+            const int r = x / (D / 4), c4 = x % (D / 4);
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < NW; ++w) {
+                const float4 y = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(smem + w * (NST * C::STAGE)) + r * D + 4 * c4);
+                v.x += y.x, v.y += y.y, v.z += y.z, v.w += y.w;
+            }
+            float m = s_m[0][r], l = 0.f;
+#pragma unroll
+            for (int w = 1; w < NW; ++w) m = fmaxf(m, s_m[w][r]);
+#pragma unroll
+            for (int w = 0; w < NW; ++w)
+                if (s_m[w][r] != -INFINITY) l += s_l[w][r] * exp2_fast(s_m[w][r] - m);
+            if (begins && ends) {
+                if (row0 + r < row1) {
+                    const float inv = l != 0.f ? 1.f / l : 0.f;
+                    store_out4(P, out_at(P, s, h, row0 + r) + 4 * c4, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+                }
+            } else {
+                *reinterpret_cast<float4 *>(part + r * D + 4 * c4) = v;
+                if (c4 == 0) {
+                    part[R * D + r] = m;
+                    part[R * D + R + r] = l;
+                }
+            }
+        }
+        if (begins && !ends && tid == 0) {
+            const long long end = at + tl.n;   // this item's last tile is end - 1
+            P.rec[blockIdx.x] = make_int4(b, h, row0, (int)((end - 1) / sh.quota));
+        }
+        tqdev::fence_proxy_async_smem();
+        __syncthreads();
+
+        // the next item
+        at += i1 - i0;
+        into = 0;
+        row0 += R;
+        if (row0 >= s.n * P.G) {
+            row0 = 0;
+            if (++h == P.Hkv) {
+                h = 0;
+                do s = load_seq(P, ++b < P.batch ? b : P.batch - 1, bad);
+                while (b < P.batch - 1 && s.n == 0);
+            }
+        }
+    }
+    // a warp that gave up waits (again with a limit) for its copies in flight
+    if (failed) {
+        atomicOr(reinterpret_cast<unsigned int *>(P.status + 1), TQ_FLAG_WAIT_TIMEOUT);
+        for (; used < filled; ++used) tqdev::mbar_wait_bounded(&bar[used % NST], (uint32_t)(used / NST) & 1u);
+    }
+}
+
+// Joins the parts of the items that were cut between CTAs.  Block x looks
+// after the item that begins in CTA x and goes on in the next (at most one),
+// rows [8 y, 8 y + 8); the threads split the parts and add them in a fixed
+// order.
+template <int D>
+__global__ void __launch_bounds__(1024) tq_paged_join_kernel(const __grid_constant__ PagedAttn P, int R) {
+    constexpr int LANES = 8 * D / 4, GROUPS = 1024 / LANES;
+    __shared__ float4 s_o[GROUPS][LANES];
+    __shared__ float s_l[GROUPS][8];
+    tqdev::grid_dep_wait();
+    if (tqdev::status_aborted(P.status)) return;
+    const int4 rec = P.rec[blockIdx.x];
+    if (rec.x < 0) return;
+    bool bad = false;
+    const Seq s = load_seq(P, rec.x, bad);
+    const int first = blockIdx.x, last = rec.w;
+    const int lane = threadIdx.x % LANES, grp = threadIdx.x / LANES;
+    const int r = blockIdx.y * 8 + lane / (D / 4), c4 = lane % (D / 4);
+    const int64_t size = (int64_t)R * (D + 2);
+    auto part = [&](int c) { return P.part + ((int64_t)c * 2 + (c == first ? 1 : 0)) * size; };
+    float m = -INFINITY;
+    for (int c = first; c <= last; ++c) m = fmaxf(m, __ldcg(part(c) + R * D + r));
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f;
+#pragma unroll 4
+    for (int c = first + grp; c <= last; c += GROUPS) {
+        const float *p = part(c);
+        const float mc = __ldcg(p + R * D + r);
+        const float f = mc == -INFINITY ? 0.f : exp2_fast(mc - m);
+        const float4 y = __ldcg(reinterpret_cast<const float4 *>(p + r * D) + c4);
+        v.x += y.x * f, v.y += y.y * f, v.z += y.z * f, v.w += y.w * f;
+        l += __ldcg(p + R * D + R + r) * f;
+    }
+    s_o[grp][lane] = v;
+    if (c4 == 0) s_l[grp][lane / (D / 4)] = l;
+    __syncthreads();
+    if (grp) return;
+    l = 0.f;
+#pragma unroll
+    for (int k = 0; k < GROUPS; ++k) l += s_l[k][lane / (D / 4)];
+#pragma unroll
+    for (int k = 1; k < GROUPS; ++k) {
+        const float4 y = s_o[k][lane];
+        v.x += y.x, v.y += y.y, v.z += y.z, v.w += y.w;
+    }
+    const int row = rec.z + r;
+    if (row >= s.n * P.G) return;
+    const float inv = l != 0.f ? 1.f / l : 0.f;
+    store_out4(P, out_at(P, s, rec.y, row) + 4 * c4, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+}
+
+template <int D, int NT>
+tq_status launch_decode(PagedAttn P, int64_t tiles_bound, int n_sms, cudaStream_t stream, size_t *need) {
+    using C = Cfg<D>;
+    constexpr int R = 8 * NT;
+    P.min_tiles = NW;
+    const int grid = (int)std::max<int64_t>(1, std::min<int64_t>((int64_t)n_sms * C::CTAS, (tiles_bound + NW - 1) / NW));
+    const size_t rec_bytes = ((size_t)grid * sizeof(int4) + 255) / 256 * 256;
+    if (need) {
+        *need = rec_bytes + (size_t)grid * 2 * R * (D + 2) * sizeof(float);
+        return TQ_OK;
+    }
+    P.rec = reinterpret_cast<int4 *>(P.part);
+    P.part = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(P.part) + rec_bytes);
+    cudaError_t e = cudaFuncSetAttribute(tq_paged_decode_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e == cudaSuccess) {
+        tq_paged_decode_kernel<D, NT><<<grid, THREADS, C::SMEM, stream>>>(P);
+        e = cudaGetLastError();
+    }
+    if (e == cudaSuccess && grid > 1)
+        e = tq_launch_dependent(tq_paged_join_kernel<D>, dim3(grid, R / 8), dim3(1024), 0, stream, P, R);
+    return tq_check_cuda(e);
+}
+
+template <int D>
+tq_status launch_dim(const PagedAttn &P, int max_q_len, int n_sms, cudaStream_t stream, size_t *need) {
+    const int64_t rows = (int64_t)max_q_len * P.G;
+    const int nt = (rows <= 8 || D == 256) ? 1 : 2;
+    const int64_t tiles = (int64_t)P.batch * P.Hkv * ((rows + 8 * nt - 1) / (8 * nt)) * (P.max_tokens / Cfg<D>::TT + 1);
+    if constexpr (D != 256)
+        if (nt == 2) return launch_decode<D, 2>(P, tiles, n_sms, stream, need);
+    return launch_decode<D, 1>(P, tiles, n_sms, stream, need);
+}
+
+}  // namespace
+
+tq_status tq_launch_paged_attention(const tq_paged *ctx, const PagedAttn &P, int max_q_len, int n_sms,
+                                    cudaStream_t stream, size_t *need) {
+    if (ctx->d == 64) return launch_dim<64>(P, max_q_len, n_sms, stream, need);
+    if (ctx->d == 128) return launch_dim<128>(P, max_q_len, n_sms, stream, need);
+    return launch_dim<256>(P, max_q_len, n_sms, stream, need);
+}
