@@ -21,7 +21,7 @@ LIB = os.path.join(OUT_DIR, "libtq.so")
 ROOT = os.path.dirname(HERE)
 
 CU_SOURCES = ["tq_api.cu", "tq_encode.cu", "tq_decode.cu", "tq_decode_mma.cu", "tq_aux.cu", "tq_static.cu", "tq_selftest.cu", "tq_split.cu",
-              "tq_paged.cu", "tq_paged_attend.cu"]
+              "tq_paged.cu", "tq_paged_attend.cu", "tq_paged_prefill.cu"]
 CPP_SOURCES = ["tq_tables.cpp"]
 HEADERS = ["tq_internal.cuh", "tq_decode.cuh", "tq_paged.cuh"]
 

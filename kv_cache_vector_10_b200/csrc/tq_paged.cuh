@@ -163,7 +163,178 @@ __device__ __forceinline__ Share find_share(const PagedAttn &P, Share *s_share, 
     return *s_share;
 }
 
+// The items (chunk of R rows of one kv head of one sequence) that a share
+// reaches, one after another, and the tiles [i0, i1) of each that are its.
+template <int R, int TT>
+struct Walk {
+    Seq s;
+    Tiles tl;
+    int b, h, row0, row1, i0, i1;
+    long long at, hi;   // tiles done, end of the share
+
+    __device__ __forceinline__ void begin(const PagedAttn &P, const Share &sh) {
+        bool bad = false;
+        b = sh.b;
+        s = load_seq(P, b, bad);
+        at = sh.lo;
+        hi = sh.hi;
+        long long into = sh.into;
+        const long long per_head = head_tiles<R, TT>(P, s);
+        h = (int)(into / per_head);
+        into -= h * per_head;
+        for (row0 = 0;; row0 += R) {
+            const int n = chunk_tiles<TT>(P, s, row0, min(s.n * P.G, row0 + R)).n;
+            if (into < n) break;
+            into -= n;
+        }
+        item(P, (int)into);
+    }
+    __device__ __forceinline__ bool more() const { return at < hi; }
+    __device__ __forceinline__ void item(const PagedAttn &P, int into) {
+        row1 = min(s.n * P.G, row0 + R);
+        tl = chunk_tiles<TT>(P, s, row0, row1);
+        i0 = into;
+        i1 = (int)min((long long)tl.n, into + (hi - at));
+    }
+    __device__ __forceinline__ void next(const PagedAttn &P) {
+        at += i1 - i0;
+        if (at >= hi) return;
+        row0 += R;
+        if (row0 >= s.n * P.G) {
+            row0 = 0;
+            if (++h == P.Hkv) {
+                h = 0;
+                bool bad = false;
+                do s = load_seq(P, ++b, bad);
+                while (s.n == 0 && b < P.batch - 1);
+            }
+        }
+        item(P, 0);
+    }
+    __device__ __forceinline__ bool begins() const { return i0 == 0; }
+    __device__ __forceinline__ bool ends() const { return i1 == tl.n; }
+    // the CTA that holds the last tile of an item that begins here
+    __device__ __forceinline__ int last_cta(const Share &sh) const { return (int)((at + tl.n - 1) / sh.quota); }
+};
+
+// Copies of one tile's codes and scales, made by one warp: lane l looks after
+// the l-th part of the tile (a page, or what of a page is in the tile).
+template <int D, int TT>
+struct TileLoad {
+    static constexpr int CODES = TT * D / 2, SCALES = TT * D / 32;
+    static constexpr int STAGE = 2 * (CODES + SCALES);   // K codes, V codes, K scales, V scales
+
+    static __device__ __forceinline__ int lg_part(const PagedAttn &P) {
+        return min(P.lg_page, TT == 128 ? 7 : TT == 64 ? 6 : 5);
+    }
+    // the page number of this lane's part of the tile at token T0, or -1
+    static __device__ __forceinline__ int fetch(const PagedAttn &P, int b, int len, int T0, int lane) {
+        const int lg = lg_part(P), tok = T0 + (lane << lg);
+        return lane < (TT >> lg) && tok < len ? __ldg(P.table + (int64_t)b * P.table_stride + (tok >> P.lg_page)) : -1;
+    }
+    // requests the tile into `dst`; returns which parts were there (a bit each)
+    static __device__ __forceinline__ uint32_t request(const PagedAttn &P, int page, int h, int len, int T0, int lane,
+                                                       uint8_t *dst, uint64_t *bar) {
+        const int lg = lg_part(P), tok = T0 + (lane << lg);
+        const bool live = lane < (TT >> lg) && tok < len;
+        const bool ok = live && page >= 0 && page < P.n_pages;
+        if (live && !ok) atomicOr(reinterpret_cast<unsigned int *>(P.status + 1), TQ_FLAG_INDEX);
+        const uint32_t got = __ballot_sync(0xffffffffu, ok);
+        const uint32_t codes = (uint32_t)(D / 2) << lg, scales = (uint32_t)(D / 32) << lg;
+        if (lane == 0) tqdev::mbar_expect_tx(bar, (uint32_t)__popc(got) * 2u * (codes + scales));
+        __syncwarp();
+        if (ok) {
+            const int64_t src = ((int64_t)page * P.Hkv + h) * P.page_bytes;
+            const int in = tok & ((1 << P.lg_page) - 1);
+            const int64_t c0 = src + (int64_t)in * (D / 2);
+            const int64_t s0 = src + ((int64_t)(D / 2) << P.lg_page) + (int64_t)in * (D / 32);
+            tqdev::bulk_load(dst + lane * codes, P.kc + c0, codes, bar);
+            tqdev::bulk_load(dst + CODES + lane * codes, P.vc + c0, codes, bar);
+            tqdev::bulk_load(dst + 2 * CODES + lane * scales, P.kc + s0, scales, bar);
+            tqdev::bulk_load(dst + 2 * CODES + SCALES + lane * scales, P.vc + s0, scales, bar);
+        }
+        return got;
+    }
+};
+
+__device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<uint32_t *>(&h); }
+__device__ __forceinline__ __half2 u2h(uint32_t u) { return *reinterpret_cast<__half2 *>(&u); }
+
+__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t bits) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "r"(mask), "r"(bits));   // (w & mask) | bits
+    return r;
+}
+
+constexpr unsigned short H_M72 = 0xD480, H_M1032 = 0xE408;   // -72 and -1032 in binary16
+
+// Pairs of codes in nibbles 0..3 of both halves of w, times the scales of
+// the two halves: p[i] = ((nibble i of the low half) - 8) s.x, the same of
+// the high half and s.y, exact.  A nibble at bit 0 of a mantissa whose last
+// place is one (1024 + c) has its 1032 taken off first (1032 s can pass the
+// largest binary16); at bit 4, with 64 + c, one operation does both, since
+// 72 s = 9 * 8 s has few bits.  m72s = -72 s.
+__device__ __forceinline__ void widen(uint32_t w, __half2 s, __half2 m72s, uint32_t (&p)[4]) {
+    const __half2 m1032 = __half2half2(__ushort_as_half(H_M1032));
+    const uint32_t w8 = w >> 8;
+    p[0] = h2u(__hmul2(__hadd2(u2h(and_or(w, 0x000F000Fu, 0x64006400u)), m1032), s));
+    p[1] = h2u(__hfma2(u2h(and_or(w, 0x00F000F0u, 0x54005400u)), s, m72s));
+    p[2] = h2u(__hmul2(__hadd2(u2h(and_or(w8, 0x000F000Fu, 0x64006400u)), m1032), s));
+    p[3] = h2u(__hfma2(u2h(and_or(w8, 0x00F000F0u, 0x54005400u)), s, m72s));
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+constexpr float RAISE = 8.f;   // the running maximum is raised when a score passes it by 2^8
+constexpr float BIAS = 6.f;    // weights are 2^(s - m + 6): at most 2^14, and exact to 2^-20
+
+// The factor (a power of two) that takes a bfloat16 row whose largest
+// magnitude has the bits `m` into binary16, to [2^14, 2^15), and its inverse.
+__device__ __forceinline__ void query_factor(uint32_t m, float &up, float &back) {
+    const int e = min(max((int)(m >> 7), 15), 254);
+    up = __uint_as_float((uint32_t)(268 - e) << 23);     // 2^(141 - e)
+    back = __uint_as_float((uint32_t)(e - 14) << 23);    // 2^(e - 141)
+}
+
+__device__ __forceinline__ uint32_t amax4(uint4 w) {
+    return __vmaxu2(__vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu), __vmaxu2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu));
+}
+
+__device__ __forceinline__ uint4 bf16_to_half(uint4 w, float up) {
+    uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        x[j] = h2u(__floats2half2_rn(__uint_as_float(x[j] << 16) * up, __uint_as_float(x[j] & 0xFFFF0000u) * up));
+    return make_uint4(x[0], x[1], x[2], x[3]);
+}
+
+// Element offsets of row `row` of (sequence, kv head) in q and in out.
+__device__ __forceinline__ int64_t query_at(const PagedAttn &P, const Seq &s, int h, int row) {
+    const int tok = row / P.G, hg = row - tok * P.G;
+    return (int64_t)(s.q0 + tok) * P.sqt + (int64_t)(h * P.G + hg) * P.sqh;
+}
+__device__ __forceinline__ int64_t out_at(const PagedAttn &P, const Seq &s, int h, int row) {
+    const int tok = row / P.G, hg = row - tok * P.G;
+    return (int64_t)(s.q0 + tok) * P.sot + (int64_t)(h * P.G + hg) * P.soh;
+}
+
+__device__ __forceinline__ uint32_t out_pair(const PagedAttn &P, float a, float b) {
+    if (P.bf16) {
+        const __nv_bfloat162 x = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&x);
+    }
+    return h2u(__floats2half2_rn(a, b));
+}
+
 }  // namespace tqpaged
 
+// Kernels of a call: for few rows (queries times heads of a group) of each kv
+// head, and for many; `need` non-null asks for the workspace's bytes only.
+tq_status tq_launch_paged_prefill(int d, const PagedAttn &P, int max_q_len, int n_sms, cudaStream_t stream, size_t *need);
+tq_status tq_launch_paged_join(int d, const PagedAttn &P, int grid, int rows, cudaStream_t stream);
 tq_status tq_launch_paged_attention(const tq_paged *ctx, const PagedAttn &P, int max_q_len, int n_sms,
                                     cudaStream_t stream, size_t *need);

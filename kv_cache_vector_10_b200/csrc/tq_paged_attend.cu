@@ -38,39 +38,16 @@ using namespace tqpaged;
 
 constexpr int NW = 4;                  // warps of a CTA
 constexpr int THREADS = 32 * NW;
-constexpr float RAISE = 8.f;           // the running maximum is raised when a score passes it by 2^8
-constexpr float BIAS = 6.f;            // weights are 2^(s - m + 6): at most 2^14, and exact to 2^-20
 
 template <int D>
 struct Cfg {
     static constexpr int TT = D == 256 ? 32 : 64;              // tokens of a tile
     static constexpr int NST = D == 64 ? 3 : 2;                // stages of a warp
     static constexpr int CTAS = D == 64 ? 4 : 3;               // CTAs of an SM
-    static constexpr int CODES = TT * D / 2, SCALES = TT * D / 32;
-    static constexpr int STAGE = 2 * (CODES + SCALES);         // K codes, V codes, K scales, V scales
+    using Load = TileLoad<D, TT>;
+    static constexpr int CODES = Load::CODES, SCALES = Load::SCALES, STAGE = Load::STAGE;
     static constexpr int SMEM = NW * NST * STAGE;
 };
-
-__device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<uint32_t *>(&h); }
-__device__ __forceinline__ __half2 u2h(uint32_t u) { return *reinterpret_cast<__half2 *>(&u); }
-
-__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t bits) {
-    uint32_t r;
-    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "r"(mask), "r"(bits));   // (w & mask) | bits
-    return r;
-}
-
-// Pairs of codes in nibbles 0..3 of both halves of w, times the scales of
-// the two halves: p[i] = ((nibble i of the low half) - 8) s.x, the same of
-// the high half and s.y.  m72s = -72 s (exact: 9 times four bits).
-__device__ __forceinline__ void widen(uint32_t w, __half2 s, __half2 m72s, uint32_t (&p)[4]) {
-    const __half2 m1032 = __half2half2(__ushort_as_half((unsigned short)0xE408));   // -1032
-    const uint32_t w8 = w >> 8;
-    p[0] = h2u(__hmul2(__hadd2(u2h(and_or(w, 0x000F000Fu, 0x64006400u)), m1032), s));
-    p[1] = h2u(__hfma2(u2h(and_or(w, 0x00F000F0u, 0x54005400u)), s, m72s));
-    p[2] = h2u(__hmul2(__hadd2(u2h(and_or(w8, 0x000F000Fu, 0x64006400u)), m1032), s));
-    p[3] = h2u(__hfma2(u2h(and_or(w8, 0x00F000F0u, 0x54005400u)), s, m72s));
-}
 
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1) {
@@ -82,12 +59,6 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     uint32_t y;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-    return y;
-}
-
-__device__ __forceinline__ float exp2_fast(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 
@@ -123,9 +94,7 @@ __device__ __forceinline__ void load_queries(const PagedAttn &P, const Seq &s, i
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) w[i] = make_uint4(0, 0, 0, 0);
         if (row < row1) {
-            const int tok = row / P.G, hg = row - tok * P.G;
-            const int64_t at = (int64_t)(s.q0 + tok) * P.sqt + (int64_t)(h * P.G + hg) * P.sqh + t * (D / 4);
-            const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(P.q) + at);
+            const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(P.q) + query_at(P, s, h, row) + t * (D / 4));
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) w[i] = __ldg(src + i);
         }
@@ -133,24 +102,14 @@ __device__ __forceinline__ void load_queries(const PagedAttn &P, const Seq &s, i
         if (P.bf16) {
             uint32_t m = 0;
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i)
-                m = __vmaxu2(m, __vmaxu2(__vmaxu2(w[i].x & 0x7FFF7FFFu, w[i].y & 0x7FFF7FFFu),
-                                         __vmaxu2(w[i].z & 0x7FFF7FFFu, w[i].w & 0x7FFF7FFFu)));
+            for (int i = 0; i < D / 32; ++i) m = __vmaxu2(m, amax4(w[i]));
             m = max(m >> 16, m & 0xFFFFu);
             m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
             m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-            // largest channel to [2^14, 2^15); the factor stays a normal float
-            const int e = min(max((int)(m >> 7), 15), 254);
-            const float up = __uint_as_float((uint32_t)(268 - e) << 23);   // 2^(141 - e)
-            back = __uint_as_float((uint32_t)(e - 14) << 23);              // 2^(e - 141)
+            float up;
+            query_factor(m, up, back);
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-                uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    x[j] = h2u(__floats2half2_rn(__uint_as_float(x[j] << 16) * up, __uint_as_float(x[j] & 0xFFFF0000u) * up));
-                w[i] = make_uint4(x[0], x[1], x[2], x[3]);
-            }
+            for (int i = 0; i < D / 32; ++i) w[i] = bf16_to_half(w[i], up);
         }
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {   // elements 0..7 of a word: pairs (0,4) (1,5) (2,6) (3,7)
@@ -165,20 +124,7 @@ __device__ __forceinline__ void load_queries(const PagedAttn &P, const Seq &s, i
 }
 
 __device__ __forceinline__ void store_out4(const PagedAttn &P, int64_t at, float4 v) {
-    uint2 o;
-    if (P.bf16) {
-        const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
-        o = make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
-    } else {
-        o = make_uint2(h2u(__floats2half2_rn(v.x, v.y)), h2u(__floats2half2_rn(v.z, v.w)));
-    }
-    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(P.out) + at) = o;
-}
-
-// Element offset of row `row` of (sequence, kv head) in the output.
-__device__ __forceinline__ int64_t out_at(const PagedAttn &P, const Seq &s, int h, int row) {
-    const int tok = row / P.G, hg = row - tok * P.G;
-    return (int64_t)(s.q0 + tok) * P.sot + (int64_t)(h * P.G + hg) * P.soh;
+    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(P.out) + at) = make_uint2(out_pair(P, v.x, v.y), out_pair(P, v.z, v.w));
 }
 
 template <int D, int NT>
@@ -210,61 +156,19 @@ __global__ void __launch_bounds__(THREADS, Cfg<D>::CTAS) tq_paged_decode_kernel(
     uint32_t valid_pages = 0;         // four bits a stage: which parts of the tile were copied
     bool failed = false;
 
-    // the place of the first tile: sequence, kv head, first row, tile
-    int b = sh.b;
-    bool bad = false;
-    Seq s = load_seq(P, b, bad);
-    int h, row0 = 0;
-    long long into = sh.into;
-    {
-        const long long per_head = head_tiles<R, TT>(P, s);
-        h = (int)(into / per_head);
-        into -= h * per_head;
-        for (;; row0 += R) {
-            const int n = chunk_tiles<TT>(P, s, row0, min(s.n * P.G, row0 + R)).n;
-            if (into < n) break;
-            into -= n;
-        }
-    }
-    long long at = sh.lo;             // tiles done
-
-    while (at < sh.hi) {
-        const int row1 = min(s.n * P.G, row0 + R);
-        const Tiles tl = chunk_tiles<TT>(P, s, row0, row1);
-        const int i0 = (int)into, i1 = (int)min((long long)tl.n, into + (sh.hi - at));
-        const int *table = P.table + (int64_t)b * P.table_stride;
-        const int lg_part = min(P.lg_page, TT == 64 ? 6 : 5), parts = TT >> lg_part;
-
-        // The page number of this lane's part of a tile, fetched one tile ahead.
-        auto fetch = [&](int i) -> int {
-            const int tok = tile_token(tl, i, TT) + (lane << lg_part);
-            return (i < i1 && lane < parts && tok < s.len) ? __ldg(table + (tok >> P.lg_page)) : -1;
-        };
+    Walk<R, TT> it;
+    for (it.begin(P, sh); it.more(); it.next(P)) {
+        const Seq &s = it.s;
+        const Tiles &tl = it.tl;
+        const int i0 = it.i0, i1 = it.i1, lg_part = C::Load::lg_part(P), parts = TT >> lg_part;
+        // page numbers are fetched one tile ahead of their use
+        auto fetch = [&](int i) { return i < i1 ? C::Load::fetch(P, it.b, s.len, tile_token(tl, i, TT), lane) : -1; };
         int next_page = fetch(i0 + warp);
         auto request = [&](int i) {
-            const int st = filled % NST;
-            const int tok = tile_token(tl, i, TT) + (lane << lg_part);
-            const int page = next_page;
+            const int st = filled % NST, page = next_page;
             next_page = fetch(i + NW);
-            const bool live = lane < parts && tok < s.len;
-            const bool ok = live && page >= 0 && page < P.n_pages;
-            if (live && !ok) atomicOr(reinterpret_cast<unsigned int *>(P.status + 1), TQ_FLAG_INDEX);
-            const uint32_t got = __ballot_sync(0xffffffffu, ok);
-            valid_pages = (valid_pages & ~(15u << (4 * st))) | ((got & 15u) << (4 * st));
-            const uint32_t codes = (uint32_t)(D / 2) << lg_part, scales = (uint32_t)(D / 32) << lg_part;
-            if (lane == 0) tqdev::mbar_expect_tx(&bar[st], (uint32_t)__popc(got) * 2u * (codes + scales));
-            __syncwarp();
-            if (ok) {
-                uint8_t *dst = ring + st * C::STAGE;
-                const int64_t src = ((int64_t)page * P.Hkv + h) * P.page_bytes;
-                const int in = tok & ((1 << P.lg_page) - 1);
-                const int64_t c0 = src + (int64_t)in * (D / 2);
-                const int64_t s0 = src + ((int64_t)(D / 2) << P.lg_page) + (int64_t)in * (D / 32);
-                tqdev::bulk_load(dst + lane * codes, P.kc + c0, codes, &bar[st]);
-                tqdev::bulk_load(dst + C::CODES + lane * codes, P.vc + c0, codes, &bar[st]);
-                tqdev::bulk_load(dst + 2 * C::CODES + lane * scales, P.kc + s0, scales, &bar[st]);
-                tqdev::bulk_load(dst + 2 * C::CODES + C::SCALES + lane * scales, P.vc + s0, scales, &bar[st]);
-            }
+            const uint32_t got = C::Load::request(P, page, it.h, s.len, tile_token(tl, i, TT), lane, ring + st * C::STAGE, &bar[st]);
+            valid_pages = (valid_pages & ~(15u << (4 * st))) | (got << (4 * st));
             ++filled;
         };
 
@@ -275,14 +179,14 @@ __global__ void __launch_bounds__(THREADS, Cfg<D>::CTAS) tq_paged_decode_kernel(
         uint32_t q[NT][D / 8];
         float mul[NT][2], m_run[NT][2], l_run[NT][2], o[NT][D / 16][4];
         int pos[NT][2];               // position of the query of column 2 t + c
-        load_queries<D, NT>(P, s, h, row0, row1, lane, q, mul);
+        load_queries<D, NT>(P, s, it.h, it.row0, it.row1, lane, q, mul);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 m_run[nt][c] = -INFINITY;
                 l_run[nt][c] = 0.f;
-                pos[nt][c] = s.len - s.n + (row0 + 8 * nt + 2 * t + c) / P.G;
+                pos[nt][c] = s.len - s.n + (it.row0 + 8 * nt + 2 * t + c) / P.G;
             }
 #pragma unroll
             for (int j = 0; j < D / 16; ++j)
@@ -322,7 +226,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<D>::CTAS) tq_paged_decode_kernel(
                     const int grp = D == 64 ? t >> 1 : D == 128 ? t : 2 * t + x / 4;
                     const __half2 s0 = u2h(ks[ra * (D / 32) + grp] * 0x00800080u);
                     const __half2 s1 = u2h(ks[rb * (D / 32) + grp] * 0x00800080u);
-                    const __half2 m72 = __half2half2(__ushort_as_half((unsigned short)0xD480));   // -72
+                    const __half2 m72 = __half2half2(__ushort_as_half(H_M72));   // -72
                     const __half2 b0 = __hmul2(s0, m72), b1 = __hmul2(s1, m72);
 #pragma unroll
                     for (int y = x; y < x + (D == 256 ? 4 : KW); ++y) {
@@ -414,7 +318,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<D>::CTAS) tq_paged_decode_kernel(
                     // rows that hold no token of this sequence may hold anything
                     if (!whole && (T0 + r >= s.len || !((got >> ((16 * u) >> lg_part)) & 1u))) sv[k] = 0;
                 }
-                const __half2 m72 = __half2half2(__ushort_as_half((unsigned short)0xD480));
+                const __half2 m72 = __half2half2(__ushort_as_half(H_M72));
                 const __half2 s0 = u2h(sv[0] * 0x80u + sv[1] * 0x800000u), s1 = u2h(sv[2] * 0x80u + sv[3] * 0x800000u);
                 const __half2 b0 = __hmul2(s0, m72), b1 = __hmul2(s1, m72);
 #pragma unroll
@@ -474,7 +378,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<D>::CTAS) tq_paged_decode_kernel(
                 }
             }
         __syncthreads();
-        const bool begins = i0 == 0, ends = i1 == tl.n;
+        const bool begins = it.begins(), ends = it.ends();
         float *part = P.part + ((int64_t)blockIdx.x * 2 + (begins ? 1 : 0)) * (R * (D + 2));
         for (int x = tid; x < R * D / 4; x += THREADS) {
             const int r = x / (D / 4), c4 = x % (D / 4);
@@ -491,9 +395,9 @@ __global__ void __launch_bounds__(THREADS, Cfg<D>::CTAS) tq_paged_decode_kernel(
             for (int w = 0; w < NW; ++w)
                 if (s_m[w][r] != -INFINITY) l += s_l[w][r] * exp2_fast(s_m[w][r] - m);
             if (begins && ends) {
-                if (row0 + r < row1) {
+                if (it.row0 + r < it.row1) {
                     const float inv = l != 0.f ? 1.f / l : 0.f;
-                    store_out4(P, out_at(P, s, h, row0 + r) + 4 * c4, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+                    store_out4(P, out_at(P, s, it.h, it.row0 + r) + 4 * c4, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
                 }
             } else {
                 *reinterpret_cast<float4 *>(part + r * D + 4 * c4) = v;
@@ -503,25 +407,9 @@ __global__ void __launch_bounds__(THREADS, Cfg<D>::CTAS) tq_paged_decode_kernel(
                 }
             }
         }
-        if (begins && !ends && tid == 0) {
-            const long long end = at + tl.n;   // this item's last tile is end - 1
-            P.rec[blockIdx.x] = make_int4(b, h, row0, (int)((end - 1) / sh.quota));
-        }
+        if (begins && !ends && tid == 0) P.rec[blockIdx.x] = make_int4(it.b, it.h, it.row0, it.last_cta(sh));
         tqdev::fence_proxy_async_smem();
         __syncthreads();
-
-        // the next item
-        at += i1 - i0;
-        into = 0;
-        row0 += R;
-        if (row0 >= s.n * P.G) {
-            row0 = 0;
-            if (++h == P.Hkv) {
-                h = 0;
-                do s = load_seq(P, ++b < P.batch ? b : P.batch - 1, bad);
-                while (b < P.batch - 1 && s.n == 0);
-            }
-        }
     }
     // a warp that gave up waits (again with a limit) for its copies in flight
     if (failed) {
@@ -599,9 +487,8 @@ tq_status launch_decode(PagedAttn P, int64_t tiles_bound, int n_sms, cudaStream_
         tq_paged_decode_kernel<D, NT><<<grid, THREADS, C::SMEM, stream>>>(P);
         e = cudaGetLastError();
     }
-    if (e == cudaSuccess && grid > 1)
-        e = tq_launch_dependent(tq_paged_join_kernel<D>, dim3(grid, R / 8), dim3(1024), 0, stream, P, R);
-    return tq_check_cuda(e);
+    if (e != cudaSuccess || grid == 1) return tq_check_cuda(e);
+    return tq_launch_paged_join(D, P, grid, R, stream);
 }
 
 template <int D>
@@ -616,8 +503,14 @@ tq_status launch_dim(const PagedAttn &P, int max_q_len, int n_sms, cudaStream_t 
 
 }  // namespace
 
+tq_status tq_launch_paged_join(int d, const PagedAttn &P, int grid, int rows, cudaStream_t stream) {
+    const auto kern = d == 64 ? tq_paged_join_kernel<64> : d == 128 ? tq_paged_join_kernel<128> : tq_paged_join_kernel<256>;
+    return tq_check_cuda(tq_launch_dependent(kern, dim3(grid, rows / 8), dim3(1024), 0, stream, P, rows));
+}
+
 tq_status tq_launch_paged_attention(const tq_paged *ctx, const PagedAttn &P, int max_q_len, int n_sms,
                                     cudaStream_t stream, size_t *need) {
+    if ((int64_t)max_q_len * P.G > 16) return tq_launch_paged_prefill(ctx->d, P, max_q_len, n_sms, stream, need);
     if (ctx->d == 64) return launch_dim<64>(P, max_q_len, n_sms, stream, need);
     if (ctx->d == 128) return launch_dim<128>(P, max_q_len, n_sms, stream, need);
     return launch_dim<256>(P, max_q_len, n_sms, stream, need);

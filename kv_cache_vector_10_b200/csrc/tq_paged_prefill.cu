@@ -1,0 +1,460 @@
+// tq_paged_prefill.cu -- attention over the paged 4-bit cache for many
+// queries a sequence (chunks of a prompt, whole prompts), on the tcgen05
+// tensor cores.  The mathematics is that of tq_paged_attend.cu.
+//
+// A CTA takes items of 128 NM rows (queries times the query heads of a kv
+// head's group) and walks the tiles of 64 tokens that they see:
+//   S[128 x 64] = Q K^T      Q in TMEM (binary16, pre-scaled rows), K in shared memory
+//   P = 2^(S - m)            one thread a row: S read from TMEM, P written over it as binary16
+//   O[128 x d] += P V        P from TMEM, V in shared memory (MN-major), O in TMEM
+// What bounds it: 4 * 64 * d operations a row and tile on the tensor cores
+// against 64 exponentials on the special-function units, which take as long
+// at d = 128; and a tile's codes have to be widened to binary16 (about 1.4
+// instructions a code), which is why two row blocks (NM = 2) share each
+// widened tile while TMEM holds both (d <= 128: 2 (d + d/2 + 64) <= 512
+// columns).  With two row blocks one is in its softmax while the other is on
+// the tensor cores; with one, two tiles' scores take turns.
+// Roles: NM x 4 softmax warps, 4 widening warps, one warp that requests the
+// codes (bulk copies of pages), one that issues the MMAs.
+#include <algorithm>
+
+#include "tq_paged.cuh"
+
+namespace {
+
+using namespace tqpaged;
+
+constexpr int PT = 64;                 // tokens of a tile
+constexpr int WIDEN_WARPS = 4;
+
+template <int D, int NM>
+struct Pre {
+    static constexpr int SOFT_WARPS = 4 * NM, THREADS = 32 * (SOFT_WARPS + WIDEN_WARPS + 2);
+    static constexpr int R = 128 * NM;
+    static constexpr int NB = D == 256 ? 2 : 3;      // widened tiles in shared memory
+    static constexpr int NC = 3;                     // code tiles in shared memory
+    using Load = TileLoad<D, PT>;
+    static constexpr int KX = PT * 128;              // 64 channels of a tile: rows of 128 bytes, swizzled
+    static constexpr int TILE = (D / 64) * KX;
+    static constexpr int OFF_V = NB * TILE, OFF_C = 2 * NB * TILE;
+    static constexpr int SMEM = OFF_C + NC * Load::STAGE + 1024;
+    // TMEM columns
+    static constexpr int COL_Q = NM * D, COL_S = COL_Q + NM * D / 2;
+    static_assert(COL_S + 2 * PT <= 512, "TMEM columns");
+    static_assert(SMEM <= 232448 - 1024, "shared memory");
+};
+
+struct PreBars {
+    uint64_t codes_full[3], codes_free[3];
+    uint64_t k_full[3], k_free[3], v_full[3], v_free[3];
+    uint64_t s_full[2], p_full[2];     // a row block's (NM = 2) or a tile parity's (NM = 1) scores, weights
+    uint64_t o_done[2], q_ready[2], done;
+};
+
+// D[tmem] (+)= A[tmem] * B[smem desc]^T, kind::f16, one CTA.
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Descriptor of an MN-major operand in 128-byte swizzled atoms: rows of 64
+// consecutive MN elements, one row per K index, 64-element MN blocks `lbo`
+// bytes apart, 8-row groups 1024 bytes apart.
+__device__ __forceinline__ uint64_t desc_mn(uint32_t saddr, uint32_t lbo) {
+    uint64_t desc = 0;
+    desc |= (uint64_t)((saddr >> 4) & 0x3FFF);
+    desc |= (uint64_t)((lbo >> 4) & 0x3FFF) << 16;
+    desc |= (uint64_t)(1024 >> 4) << 32;
+    desc |= (uint64_t)1 << 46;
+    desc |= (uint64_t)2 << 61;
+    return desc;
+}
+
+__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t phase) {
+    return __all_sync(0xffffffffu, tqdev::mbar_wait_bounded(bar, phase));
+}
+
+// Bit c of the result: token T0 + c is seen from position p.
+__device__ __forceinline__ uint64_t seen_bits(const PagedAttn &P, int T0, int p, uint32_t got, int lg_part) {
+    const int hi = p - T0;
+    uint64_t see = hi < 0 ? 0ull : hi >= 63 ? ~0ull : (2ull << hi) - 1ull;
+    if (P.window > 0) {
+        const int lo = p - P.window + 1 - T0, ns = P.sinks - T0;
+        const uint64_t win = lo <= 0 ? ~0ull : lo >= 64 ? 0ull : ~0ull << lo;
+        see &= win | (ns <= 0 ? 0ull : ns >= 64 ? ~0ull : (1ull << ns) - 1ull);
+    }
+    const uint64_t part = lg_part >= 6 ? ~0ull : (1ull << (1 << lg_part)) - 1ull;
+    for (int j = 0; j < (PT >> lg_part); ++j)
+        if (!((got >> j) & 1u)) see &= ~(part << (j << lg_part));
+    return see;
+}
+
+template <int D, int NM>
+__global__ void __launch_bounds__(Pre<D, NM>::THREADS, 1) tq_paged_prefill_kernel(const __grid_constant__ PagedAttn P) {
+    using C = Pre<D, NM>;
+    constexpr int NB = C::NB, NC = C::NC, R = C::R, SW = C::SOFT_WARPS;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    __shared__ __align__(8) PreBars bars;
+    __shared__ Share s_share;
+    __shared__ long long s_sum[C::THREADS / 32];
+    __shared__ uint32_t s_tmem, s_valid[16];   // s_valid: which parts of a tile were there, 16 tiles back
+    __shared__ int s_abort;
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    tqdev::grid_dep_trigger();
+    if (tid == 0) {
+        for (int i = 0; i < 3; ++i) {
+            tqdev::mbar_init(&bars.codes_full[i], 1);
+            tqdev::mbar_init(&bars.codes_free[i], WIDEN_WARPS);
+            tqdev::mbar_init(&bars.k_full[i], WIDEN_WARPS);
+            tqdev::mbar_init(&bars.k_free[i], 1);
+            tqdev::mbar_init(&bars.v_full[i], WIDEN_WARPS);
+            tqdev::mbar_init(&bars.v_free[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            tqdev::mbar_init(&bars.s_full[i], 1);
+            tqdev::mbar_init(&bars.p_full[i], 4);
+            tqdev::mbar_init(&bars.o_done[i], 1);
+            tqdev::mbar_init(&bars.q_ready[i], 4);
+        }
+        tqdev::mbar_init(&bars.done, 1);
+        s_abort = tqdev::status_aborted(P.status) ? 1 : 0;
+        P.rec[blockIdx.x] = make_int4(-1, 0, 0, 0);
+        tqdev::fence_barrier_init();
+    }
+    const Share sh = find_share<R, PT, C::THREADS>(P, &s_share, s_sum);
+    if (s_abort || sh.lo >= sh.hi) return;
+    if (warp == 0) tqdev::tmem_alloc(&s_tmem, 512);
+    tqdev::tc_fence_before();
+    __syncthreads();
+    tqdev::tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    const int lg_part = C::Load::lg_part(P), parts = PT >> lg_part;
+    const uint32_t all_parts = (1u << parts) - 1u;
+    bool failed = false;
+    Walk<R, PT> it;
+
+    if (warp < SW) {
+        // ------------------------------------------------------------- softmax
+        const int m = warp >> 2, r = 128 * m + 32 * (warp & 3) + lane;
+        const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+        const uint32_t t_o = lanes + m * D, t_q = lanes + C::COL_Q + m * (D / 2);
+        int n = 0;
+        for (it.begin(P, sh); it.more() && !failed; it.next(P)) {
+            const Seq &s = it.s;
+            const int row = it.row0 + r;
+            const bool active = row < it.row1;
+            const int pos = s.len - s.n + row / P.G;
+            // positions of the first and last query of this row block
+            const int p_lo = s.len - s.n + (it.row0 + 128 * m) / P.G;
+            const int p_hi = s.len - s.n + (it.row0 + 128 * m + 127) / P.G;
+
+            // this row's query: binary16, channels in the order of widen()
+            const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(P.q) + (active ? query_at(P, s, it.h, row) : 0));
+            float up = 1.f, mul = 1.f;
+            if (P.bf16 && active) {
+                uint32_t a = 0;
+#pragma unroll 8
+                for (int i = 0; i < D / 8; ++i) a = __vmaxu2(a, amax4(__ldg(src + i)));
+                query_factor(max(a >> 16, a & 0xFFFFu), up, mul);
+            }
+            mul *= P.scale_log2;
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) {
+                float x[32];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    uint4 w = active ? __ldg(src + 8 * c + i) : make_uint4(0, 0, 0, 0);
+                    if (P.bf16) w = bf16_to_half(w, up);
+                    x[4 * i + 0] = __uint_as_float(__byte_perm(w.x, w.z, 0x5410));
+                    x[4 * i + 1] = __uint_as_float(__byte_perm(w.x, w.z, 0x7632));
+                    x[4 * i + 2] = __uint_as_float(__byte_perm(w.y, w.w, 0x5410));
+                    x[4 * i + 3] = __uint_as_float(__byte_perm(w.y, w.w, 0x7632));
+                }
+                tqdev::tmem_st_32x32b_x32(t_q + 32 * c, x);
+            }
+            tqdev::tmem_wait_st();
+            tqdev::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) tqdev::mbar_arrive(&bars.q_ready[m]);
+
+            float m_run = -INFINITY, l_run = 0.f;
+            for (int i = it.i0; i < it.i1; ++i, ++n) {
+                const int buf = NM == 2 ? m : n & 1;
+                const uint32_t ph = NM == 2 ? n & 1 : (n >> 1) & 1;
+                const uint32_t t_s = lanes + C::COL_S + buf * PT;
+                if (!wait_warp(&bars.s_full[buf], ph)) {
+                    failed = true;
+                    break;
+                }
+                tqdev::tc_fence_after();
+                float x[2][32];
+                tqdev::tmem_ld_32x32b_x32_nowait(t_s, x[0]);
+                tqdev::tmem_ld_32x32b_x32(t_s + 32, x[1]);
+                const int T0 = tile_token(it.tl, i, PT);
+                const uint32_t got = *reinterpret_cast<volatile uint32_t *>(&s_valid[n & 15]);
+                const bool whole = T0 + PT - 1 <= p_lo && (P.window <= 0 || T0 > p_hi - P.window || T0 + PT <= P.sinks) && got == all_parts;
+                if (!whole) {
+                    const uint64_t see = seen_bits(P, T0, pos, got, lg_part);
+                    const uint32_t lo = (uint32_t)see, hi = (uint32_t)(see >> 32);
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) {
+                        if (!((lo >> c) & 1u)) x[0][c] = -INFINITY;
+                        if (!((hi >> c) & 1u)) x[1][c] = -INFINITY;
+                    }
+                }
+                float mx = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < 32; ++c) mx = fmaxf(mx, fmaxf(x[0][c], x[1][c]));
+                mx *= mul;
+                const bool raise = mx > m_run + RAISE;
+                if (__any_sync(0xffffffffu, raise)) {
+                    const float to = fmaxf(m_run, mx);
+                    const float f = m_run == -INFINITY ? 0.f : exp2_fast(m_run - to);
+                    m_run = to;
+                    l_run *= f;
+                    if (i > it.i0) {   // the output of the tiles before, once it is complete
+                        if (!wait_warp(&bars.o_done[m], (uint32_t)(n - 1) & 1u)) {
+                            failed = true;
+                            break;
+                        }
+                        tqdev::tc_fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 32) {
+                            float o[32];
+                            tqdev::tmem_ld_32x32b_x32(t_o + c, o);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] *= f;
+                            tqdev::tmem_st_32x32b_x32(t_o + c, o);
+                        }
+                    }
+                }
+                const float ref = m_run == -INFINITY ? 0.f : m_run - BIAS;
+                float w[32], l0 = 0.f, l1 = 0.f;
+#pragma unroll
+                for (int c = 0; c < 32; ++c) {
+                    const float a = exp2_fast(fmaf(x[c >> 4][2 * (c & 15)], mul, -ref));
+                    const float b = exp2_fast(fmaf(x[c >> 4][2 * (c & 15) + 1], mul, -ref));
+                    l0 += a;
+                    l1 += b;
+                    w[c] = __uint_as_float(h2u(__floats2half2_rn(a, b)));
+                }
+                l_run += l0 + l1;
+                tqdev::tmem_st_32x32b_x32(t_s, w);
+                tqdev::tmem_wait_st();
+                tqdev::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) tqdev::mbar_arrive(&bars.p_full[buf]);
+            }
+            if (failed) break;
+            // the item's rows, or this CTA's part of them
+            if (!wait_warp(&bars.o_done[m], (uint32_t)(n - 1) & 1u)) {
+                failed = true;
+                break;
+            }
+            tqdev::tc_fence_after();
+            const bool direct = it.begins() && it.ends();
+            const float inv = !direct ? 1.f : l_run != 0.f ? 1.f / l_run : 0.f;
+            uint16_t *out = static_cast<uint16_t *>(P.out) + (active ? out_at(P, s, it.h, row) : 0);
+            float *part = P.part + ((int64_t)blockIdx.x * 2 + (it.begins() ? 1 : 0)) * (R * (D + 2));
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+                float o[32];
+                tqdev::tmem_ld_32x32b_x32(t_o + c, o);
+#pragma unroll
+                for (int e = 0; e < 32; e += 8) {   // columns 0..7 hold channels 0 4 1 5 2 6 3 7
+                    const float4 a = make_float4(o[e] * inv, o[e + 2] * inv, o[e + 4] * inv, o[e + 6] * inv);
+                    const float4 b = make_float4(o[e + 1] * inv, o[e + 3] * inv, o[e + 5] * inv, o[e + 7] * inv);
+                    if (!direct) {
+                        *reinterpret_cast<float4 *>(part + (int64_t)r * D + c + e) = a;
+                        *reinterpret_cast<float4 *>(part + (int64_t)r * D + c + e + 4) = b;
+                    } else if (active) {
+                        *reinterpret_cast<uint4 *>(out + c + e) =
+                            make_uint4(out_pair(P, a.x, a.y), out_pair(P, a.z, a.w), out_pair(P, b.x, b.y), out_pair(P, b.z, b.w));
+                    }
+                }
+            }
+            if (!direct) {
+                part[R * D + r] = m_run;
+                part[R * D + R + r] = l_run;
+                if (it.begins() && tid == 0) P.rec[blockIdx.x] = make_int4(it.b, it.h, it.row0, it.last_cta(sh));
+            }
+            tqdev::tc_fence_before();
+        }
+    } else if (warp < SW + WIDEN_WARPS) {
+        // ------------------------------------------------------------ widening
+        // A lane takes a group (32 channels) of a token: sixteen bytes of
+        // codes to four swizzled sixteen-byte chunks an operand row.  The
+        // lanes of a quarter warp take two groups of four tokens, so that
+        // their chunks fall into different banks.
+        const int e = warp - SW;
+        const int sub = lane & 1, tr = 16 * e + (lane >> 1);   // token row of this lane, every tile
+        int n = 0;
+        for (it.begin(P, sh); it.more() && !failed; it.next(P)) {
+            for (int i = it.i0; i < it.i1; ++i, ++n) {
+                const int cs = n % NC, b = n % NB;
+                if (!wait_warp(&bars.codes_full[cs], (uint32_t)(n / NC) & 1u)) {
+                    failed = true;
+                    break;
+                }
+                const uint8_t *codes = sm + C::OFF_C + cs * C::Load::STAGE;
+                const uint8_t *scales = codes + 2 * C::Load::CODES;
+                const uint32_t got = *reinterpret_cast<volatile uint32_t *>(&s_valid[n & 15]);
+                // a row that holds no token of this sequence may hold anything
+                const bool there = tile_token(it.tl, i, PT) + tr < it.s.len && ((got >> (tr >> lg_part)) & 1u);
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv) {
+                    if (n >= NB && !wait_warp(kv ? &bars.v_free[b] : &bars.k_free[b], (uint32_t)(n / NB - 1) & 1u)) {
+                        failed = true;
+                        break;
+                    }
+                    uint8_t *dst = sm + (kv ? C::OFF_V : 0) + b * C::TILE + tr * 128;
+#pragma unroll
+                    for (int blk = 0; blk < D / 64; ++blk) {
+                        const int grp = 2 * blk + sub;
+                        const uint4 w = *reinterpret_cast<const uint4 *>(codes + kv * C::Load::CODES + tr * (D / 2) + grp * 16);
+                        const uint32_t sb = there ? scales[kv * C::Load::SCALES + tr * (D / 32) + grp] : 0u;
+                        const __half2 sc = u2h(sb * 0x00800080u);
+                        const __half2 m72s = __hmul2(sc, __half2half2(__ushort_as_half(H_M72)));
+                        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            uint32_t p[4];
+                            widen(ws[j], sc, m72s, p);
+                            *reinterpret_cast<uint4 *>(dst + blk * C::KX + (((4 * sub + j) ^ (tr & 7)) << 4)) =
+                                make_uint4(p[0], p[1], p[2], p[3]);
+                        }
+                    }
+                    tqdev::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) tqdev::mbar_arrive(kv ? &bars.v_full[b] : &bars.k_full[b]);
+                }
+                if (failed) break;
+                if (lane == 0) tqdev::mbar_arrive(&bars.codes_free[cs]);
+            }
+        }
+    } else if (warp == SW + WIDEN_WARPS) {
+        // ------------------------------------------------- requests of the codes
+        int n = 0;
+        for (it.begin(P, sh); it.more() && !failed; it.next(P)) {
+            int page = C::Load::fetch(P, it.b, it.s.len, tile_token(it.tl, it.i0, PT), lane);
+            for (int i = it.i0; i < it.i1; ++i, ++n) {
+                const int cs = n % NC;
+                const int next = i + 1 < it.i1 ? C::Load::fetch(P, it.b, it.s.len, tile_token(it.tl, i + 1, PT), lane) : -1;
+                if (n >= NC && !wait_warp(&bars.codes_free[cs], (uint32_t)(n / NC - 1) & 1u)) {
+                    failed = true;
+                    break;
+                }
+                // the parts are known before the copies that announce them
+                const int tok = tile_token(it.tl, i, PT) + (lane << lg_part);
+                const uint32_t got = __ballot_sync(0xffffffffu, lane < parts && tok < it.s.len && page >= 0 && page < P.n_pages);
+                if (lane == 0) *reinterpret_cast<volatile uint32_t *>(&s_valid[n & 15]) = got;
+                __syncwarp();
+                C::Load::request(P, page, it.h, it.s.len, tile_token(it.tl, i, PT), lane, sm + C::OFF_C + cs * C::Load::STAGE,
+                                 &bars.codes_full[cs]);
+                page = next;
+            }
+        }
+        // whatever happened to the others: the copies in flight have landed
+        for (int k = max(0, n - NC); k < n; ++k) tqdev::mbar_wait_bounded(&bars.codes_full[k % NC], (uint32_t)(k / NC) & 1u);
+    } else if (lane == 0) {
+        // ----------------------------------------------------------------- MMAs
+        const uint32_t id_s = tqdev::idesc_f16_f32(PT), id_o = tqdev::idesc_f16_f32(D) | (1u << 16);   // V is MN-major
+        const uint32_t k0 = tqdev::smem_u32(sm), v0 = k0 + C::OFF_V;
+        auto scores = [&](int kn, int m, int buf) {
+            const uint32_t kb = k0 + (uint32_t)((kn % NB) * C::TILE);
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks)
+                mma_ts(tmem + C::COL_S + buf * PT, tmem + C::COL_Q + m * (D / 2) + 8 * ks,
+                       tqdev::smem_desc_sw128(kb + (ks >> 2) * C::KX + (ks & 3) * 32), id_s, ks != 0);
+            tqdev::mma_commit(&bars.s_full[buf]);
+        };
+        auto outputs = [&](int vn, int m, int buf, bool first) {
+            const uint32_t vb = v0 + (uint32_t)((vn % NB) * C::TILE);
+#pragma unroll
+            for (int ks = 0; ks < PT / 16; ++ks)
+                mma_ts(tmem + m * D, tmem + C::COL_S + buf * PT + 8 * ks, desc_mn(vb + 2048 * ks, C::KX), id_o, !(first && ks == 0));
+            tqdev::mma_commit(&bars.o_done[m]);
+        };
+        auto wait_k = [&](int kn) {
+            const bool ok = tqdev::mbar_wait_bounded(&bars.k_full[kn % NB], (uint32_t)(kn / NB) & 1u);
+            tqdev::tc_fence_after();
+            return ok;
+        };
+        int n = 0, items = 0;
+        bool ok = true;
+        for (it.begin(P, sh); it.more() && ok; it.next(P), ++items) {
+            const int nt = it.i1 - it.i0;
+            for (int m = 0; m < NM && ok; ++m) ok = tqdev::mbar_wait_bounded(&bars.q_ready[m], (uint32_t)items & 1u);
+            for (int j = 0; j < (NM == 2 ? 1 : 2) && j < nt && ok; ++j) {
+                if (!(ok = wait_k(n + j))) break;
+                for (int m = 0; m < NM; ++m) scores(n + j, m, NM == 2 ? m : (n + j) & 1);
+                tqdev::mma_commit(&bars.k_free[(n + j) % NB]);
+            }
+            for (int i = 0; i < nt && ok; ++i, ++n) {
+                for (int m = 0; m < NM && ok; ++m) {
+                    const int buf = NM == 2 ? m : n & 1;
+                    ok = tqdev::mbar_wait_bounded(&bars.p_full[buf], NM == 2 ? (uint32_t)n & 1u : (uint32_t)(n >> 1) & 1u) &&
+                         (m > 0 || tqdev::mbar_wait_bounded(&bars.v_full[n % NB], (uint32_t)(n / NB) & 1u));
+                    if (!ok) break;
+                    tqdev::tc_fence_after();
+                    outputs(n, m, buf, i == 0);
+                    const int ahead = NM == 2 ? 1 : 2;
+                    if (i + ahead < nt) {
+                        if (m == 0 && !(ok = wait_k(n + ahead))) break;
+                        scores(n + ahead, m, buf);
+                    }
+                }
+                if (!ok) break;
+                tqdev::mma_commit(&bars.v_free[n % NB]);
+                const int ahead = NM == 2 ? 1 : 2;
+                if (i + ahead < nt) tqdev::mma_commit(&bars.k_free[(n + ahead) % NB]);
+            }
+        }
+        failed = !ok;
+        tqdev::mma_commit(&bars.done);
+        if (!tqdev::mbar_wait_bounded(&bars.done, 0u)) failed = true;
+    }
+    if (failed) atomicOr(reinterpret_cast<unsigned int *>(P.status + 1), TQ_FLAG_WAIT_TIMEOUT);
+    tqdev::tc_fence_before();
+    __syncthreads();
+    tqdev::tc_fence_after();
+    if (warp == 0) tqdev::tmem_dealloc(tmem, 512);
+}
+
+template <int D, int NM>
+tq_status launch_prefill(PagedAttn P, int64_t tiles_bound, int n_sms, cudaStream_t stream, size_t *need) {
+    using C = Pre<D, NM>;
+    P.min_tiles = 4;
+    const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(n_sms, (tiles_bound + P.min_tiles - 1) / P.min_tiles));
+    const size_t rec_bytes = ((size_t)grid * sizeof(int4) + 255) / 256 * 256;
+    if (need) {
+        *need = rec_bytes + (size_t)grid * 2 * C::R * (D + 2) * sizeof(float);
+        return TQ_OK;
+    }
+    P.rec = reinterpret_cast<int4 *>(P.part);
+    P.part = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(P.part) + rec_bytes);
+    cudaError_t e = cudaFuncSetAttribute(tq_paged_prefill_kernel<D, NM>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e == cudaSuccess) {
+        tq_paged_prefill_kernel<D, NM><<<grid, C::THREADS, C::SMEM, stream>>>(P);
+        e = cudaGetLastError();
+    }
+    if (e != cudaSuccess || grid == 1) return tq_check_cuda(e);
+    return tq_launch_paged_join(D, P, grid, C::R, stream);
+}
+
+}  // namespace
+
+tq_status tq_launch_paged_prefill(int d, const PagedAttn &P, int max_q_len, int n_sms, cudaStream_t stream, size_t *need) {
+    const int64_t rows = (int64_t)max_q_len * P.G;
+    const int nm = rows > 128 && d != 256 ? 2 : 1;
+    const int64_t tiles = (int64_t)P.batch * P.Hkv * ((rows + 128 * nm - 1) / (128 * nm)) * (P.max_tokens / PT + 1);
+    if (d == 64) return nm == 2 ? launch_prefill<64, 2>(P, tiles, n_sms, stream, need) : launch_prefill<64, 1>(P, tiles, n_sms, stream, need);
+    if (d == 128) return nm == 2 ? launch_prefill<128, 2>(P, tiles, n_sms, stream, need) : launch_prefill<128, 1>(P, tiles, n_sms, stream, need);
+    return launch_prefill<256, 1>(P, tiles, n_sms, stream, need);
+}

@@ -461,3 +461,39 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for i in range(2):
         assert all(torch.equal(o, want[i]) for o in got[i])
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("d,H,G,page,lens,new", [(64, 1, 1, 64, [64], [64]), (128, 2, 4, 64, [200], [33]), (128, 1, 8, 16, [300, 17], [40, 17]),
+                                                 (64, 2, 3, 128, [500, 20, 129], [500, 20, 1]), (256, 1, 4, 32, [333, 90], [90, 77]),
+                                                 (128, 1, 1, 256, [700], [699])])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (70, 5)])
+def test_prompts(dtype, d, H, G, page, lens, new, window, sinks):
+    """Many queries a sequence: chunks and whole prompts on the tensor cores."""
+    starts = np.concatenate(([0], np.cumsum(new)))
+    cache, table, lens_t, g = _pool(lens, H, d, page, seed=d + G + page, dtype=dtype)
+    q = _randn(g, int(starts[-1]), H * G, d, dtype=dtype)
+    st = torch.tensor(starts, dtype=torch.int32, device=DEV)
+    out = cache.attention(q, table, lens_t, q_starts=st, max_q_len=max(new), window=window, sinks=sinks)
+    _check(cache, q, table, lens_t, starts, out, window=window, sinks=sinks)
+    assert torch.equal(out, cache.attention(q, table, lens_t, q_starts=st, max_q_len=max(new), window=window, sinks=sinks))
+    assert cache.status() == (0, 0)
+
+
+def test_long_prompt_chunk_split_over_the_gpu():
+    cache, table, lens_t, g = _pool([6000], 1, 128, 64, seed=77)
+    q = _randn(g, 90, 4, 128, dtype=torch.bfloat16)
+    st = torch.tensor([0, 90], dtype=torch.int32, device=DEV)
+    out = cache.attention(q, table, lens_t, q_starts=st, max_q_len=90)
+    _check(cache, q, table, lens_t, np.array([0, 90]), out)
+    assert torch.equal(out, cache.attention(q, table, lens_t, q_starts=st, max_q_len=90))
+
+
+def test_prompt_scores_far_apart():
+    """The running maximum moves late and by much: the outputs so far are
+    scaled down, rows of one warp by unlike factors."""
+    cache, table, lens_t, g = _pool([800], 1, 128, 64, seed=78)
+    q = _randn(g, 200, 1, 128, dtype=torch.float16) * torch.linspace(0.01, 60, 200, device=DEV)[:, None, None].half()
+    st = torch.tensor([0, 200], dtype=torch.int32, device=DEV)
+    out = cache.attention(q, table, lens_t, q_starts=st, max_q_len=200)
+    _check(cache, q, table, lens_t, np.array([0, 200]), out)
