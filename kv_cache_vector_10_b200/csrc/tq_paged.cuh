@@ -42,7 +42,7 @@ struct PagedAttn {
     int window, sinks;
     float scale_log2;                // softmax scale times log2(e)
     float *part;                     // split partials: [2 * grid][rows (d + 2)]
-    int4 *rec;                       // [grid]: the split item that begins in this CTA
+    void *rec;                       // [grid] tqpaged::Joint
     unsigned long long *status;
     int min_tiles;                   // least tiles a CTA takes
 };
@@ -149,8 +149,9 @@ __device__ __forceinline__ Share find_share(const PagedAttn &P, Share *s_share, 
     if (tid == 0) *s_share = Share{lo, hi, quota, P.batch, 0};
     __syncthreads();
     if (lo < hi && mine > 0 && lo >= first && lo < first + mine) {
+        if (per == 1) *s_share = Share{lo, hi, quota, b0, lo - first};
         long long at = first;
-        for (int b = b0; b < b1; ++b) {
+        for (int b = b0; per > 1 && b < b1; ++b) {
             const long long t = head_tiles<R, TT>(P, load_seq(P, b, bad)) * P.Hkv;
             if (lo < at + t) {
                 *s_share = Share{lo, hi, quota, b, lo - at};
@@ -162,6 +163,13 @@ __device__ __forceinline__ Share find_share(const PagedAttn &P, Share *s_share, 
     __syncthreads();
     return *s_share;
 }
+
+// A CTA's note for the joining kernel: the item that it took over from the
+// CTA before it, if any.
+struct Joint {
+    int row0, rows, first, last;   // rows <= 0: none; CTAs that hold parts of it
+    long long q0, h;               // its sequence's first query row, its kv head
+};
 
 // The items (chunk of R rows of one kv head of one sequence) that a share
 // reaches, one after another, and the tiles [i0, i1) of each that are its.
@@ -180,7 +188,7 @@ struct Walk {
         hi = sh.hi;
         long long into = sh.into;
         const long long per_head = head_tiles<R, TT>(P, s);
-        h = (int)(into / per_head);
+        h = (into | per_head) >> 32 ? (int)(into / per_head) : (int)((uint32_t)into / (uint32_t)per_head);
         into -= h * per_head;
         for (row0 = 0;; row0 += R) {
             const int n = chunk_tiles<TT>(P, s, row0, min(s.n * P.G, row0 + R)).n;
@@ -213,47 +221,70 @@ struct Walk {
     }
     __device__ __forceinline__ bool begins() const { return i0 == 0; }
     __device__ __forceinline__ bool ends() const { return i1 == tl.n; }
-    // the CTA that holds the last tile of an item that begins here
-    __device__ __forceinline__ int last_cta(const Share &sh) const { return (int)((at + tl.n - 1) / sh.quota); }
+    // the note on this share's first item
+    __device__ __forceinline__ Joint joint(const Share &sh) const {
+        const long long start = at - i0;
+        return Joint{row0, begins() ? 0 : row1 - row0, (int)(start / sh.quota), (int)((start + tl.n - 1) / sh.quota), s.q0, h};
+    }
 };
 
-// Copies of one tile's codes and scales, made by one warp: lane l looks after
-// the l-th part of the tile (a page, or what of a page is in the tile).
-template <int D, int TT>
+// Copies of the codes and scales of TILES tiles, made by one warp: a lane
+// looks after a part of a tile (a page, or what of a page is in the tile).
+template <int D, int TT, int TILES>
 struct TileLoad {
-    static constexpr int CODES = TT * D / 2, SCALES = TT * D / 32;
-    static constexpr int STAGE = 2 * (CODES + SCALES);   // K codes, V codes, K scales, V scales
+    static constexpr int SIDE = TT * (D / 2 + D / 32);   // keys, then values: each part's codes, then its scales
+    static constexpr int TILE = 2 * SIDE, STAGE = TILES * TILE;
+    static_assert(TILES * TT / 16 <= 32, "a lane for each part");
 
-    static __device__ __forceinline__ int lg_part(const PagedAttn &P) {
-        return min(P.lg_page, TT == 128 ? 7 : TT == 64 ? 6 : 5);
+    int lg, parts, tile, part;   // tokens of a part (log2), parts of a tile; this lane's
+
+    __device__ __forceinline__ TileLoad(const PagedAttn &P, int lane) {
+        lg = min(P.lg_page, TT == 64 ? 6 : 5);
+        parts = TT >> lg;
+        tile = lane / parts;
+        part = lane % parts;
     }
-    // the page number of this lane's part of the tile at token T0, or -1
-    static __device__ __forceinline__ int fetch(const PagedAttn &P, int b, int len, int T0, int lane) {
-        const int lg = lg_part(P), tok = T0 + (lane << lg);
-        return lane < (TT >> lg) && tok < len ? __ldg(P.table + (int64_t)b * P.table_stride + (tok >> P.lg_page)) : -1;
+    // the token at which this lane's part begins, tiles from i on of [.., i1); -1 for none
+    __device__ __forceinline__ int token(const Tiles &t, int i, int i1, int len) const {
+        const int tok = tile_token(t, i + tile, TT) + (part << lg);
+        return tile < TILES && i + tile < i1 && tok < len ? tok : -1;
     }
-    // requests the tile into `dst`; returns which parts were there (a bit each)
-    static __device__ __forceinline__ uint32_t request(const PagedAttn &P, int page, int h, int len, int T0, int lane,
-                                                       uint8_t *dst, uint64_t *bar) {
-        const int lg = lg_part(P), tok = T0 + (lane << lg);
-        const bool live = lane < (TT >> lg) && tok < len;
-        const bool ok = live && page >= 0 && page < P.n_pages;
-        if (live && !ok) atomicOr(reinterpret_cast<unsigned int *>(P.status + 1), TQ_FLAG_INDEX);
+    static __device__ __forceinline__ int fetch(const PagedAttn &P, int b, int tok) {
+        return tok < 0 ? -1 : __ldg(P.table + (int64_t)b * P.table_stride + (tok >> P.lg_page));
+    }
+    // Requests the tiles into `dst`, their parts that are there into *valid
+    // (a bit each, tile by tile) before that.
+    __device__ __forceinline__ void request(const PagedAttn &P, int tok, int page, int h, int lane, uint8_t *dst,
+                                            volatile uint32_t *valid, uint64_t *bar) const {
+        const bool ok = tok >= 0 && page >= 0 && page < P.n_pages;
+        if (tok >= 0 && !ok) atomicOr(reinterpret_cast<unsigned int *>(P.status + 1), TQ_FLAG_INDEX);
         const uint32_t got = __ballot_sync(0xffffffffu, ok);
         const uint32_t codes = (uint32_t)(D / 2) << lg, scales = (uint32_t)(D / 32) << lg;
-        if (lane == 0) tqdev::mbar_expect_tx(bar, (uint32_t)__popc(got) * 2u * (codes + scales));
-        __syncwarp();
-        if (ok) {
-            const int64_t src = ((int64_t)page * P.Hkv + h) * P.page_bytes;
-            const int in = tok & ((1 << P.lg_page) - 1);
-            const int64_t c0 = src + (int64_t)in * (D / 2);
-            const int64_t s0 = src + ((int64_t)(D / 2) << P.lg_page) + (int64_t)in * (D / 32);
-            tqdev::bulk_load(dst + lane * codes, P.kc + c0, codes, bar);
-            tqdev::bulk_load(dst + CODES + lane * codes, P.vc + c0, codes, bar);
-            tqdev::bulk_load(dst + 2 * CODES + lane * scales, P.kc + s0, scales, bar);
-            tqdev::bulk_load(dst + 2 * CODES + SCALES + lane * scales, P.vc + s0, scales, bar);
+        if (lane == 0) {
+            *valid = got;
+            tqdev::mbar_expect_tx(bar, (uint32_t)__popc(got) * 2u * (codes + scales));
         }
-        return got;
+        __syncwarp();
+        if (!ok) return;
+        const int64_t src = ((int64_t)page * P.Hkv + h) * P.page_bytes;
+        dst += tile * TILE + part * (codes + scales);
+        if (P.lg_page == lg) {   // a whole page: codes and scales in one piece
+            tqdev::bulk_load(dst, P.kc + src, codes + scales, bar);
+            tqdev::bulk_load(dst + SIDE, P.vc + src, codes + scales, bar);
+            return;
+        }
+        const int in = tok & ((1 << P.lg_page) - 1);
+        const int64_t c0 = src + (int64_t)in * (D / 2);
+        const int64_t s0 = src + ((int64_t)(D / 2) << P.lg_page) + (int64_t)in * (D / 32);
+        tqdev::bulk_load(dst, P.kc + c0, codes, bar);
+        tqdev::bulk_load(dst + codes, P.kc + s0, scales, bar);
+        tqdev::bulk_load(dst + SIDE, P.vc + c0, codes, bar);
+        tqdev::bulk_load(dst + SIDE + codes, P.vc + s0, scales, bar);
+    }
+    // byte offsets in a side of token r's codes and scales
+    static __device__ __forceinline__ int codes_at(int r, int lg) { return r * (D / 2) + ((r >> lg) << lg) * (D / 32); }
+    static __device__ __forceinline__ int scales_at(int r, int lg) {
+        return (((r >> lg) + 1) << lg) * (D / 2) + r * (D / 32);
     }
 };
 
@@ -266,21 +297,32 @@ __device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t b
     return r;
 }
 
-constexpr unsigned short H_M72 = 0xD480, H_M1032 = 0xE408;   // -72 and -1032 in binary16
+// A scale as widen() takes it, two of them side by side (w: a scale byte in
+// the low bits of each half).  Everything is 2^-7 of its true size: then
+// 1032 s fits binary16 for every scale, and every value below is still exact,
+// a multiple of 2^-24 with at most eleven bits.
+struct Scale2 {
+    __half2 s, m1032, m72;   // s, -1032 s, -72 s
+};
+constexpr float WIDE = 128.f;   // what widened values have to be multiplied by
+
+__device__ __forceinline__ Scale2 scale2(uint32_t w) {
+    const __half2 v = u2h(w << 7);
+    return {__hmul2(v, __float2half2_rn(0.0078125f)), __hmul2(v, __float2half2_rn(-8.0625f)),
+            __hmul2(v, __float2half2_rn(-0.5625f))};
+}
 
 // Pairs of codes in nibbles 0..3 of both halves of w, times the scales of
-// the two halves: p[i] = ((nibble i of the low half) - 8) s.x, the same of
-// the high half and s.y, exact.  A nibble at bit 0 of a mantissa whose last
-// place is one (1024 + c) has its 1032 taken off first (1032 s can pass the
-// largest binary16); at bit 4, with 64 + c, one operation does both, since
-// 72 s = 9 * 8 s has few bits.  m72s = -72 s.
-__device__ __forceinline__ void widen(uint32_t w, __half2 s, __half2 m72s, uint32_t (&p)[4]) {
-    const __half2 m1032 = __half2half2(__ushort_as_half(H_M1032));
+// the two halves: p[i] = 2^-7 ((nibble i of the low half) - 8) s.x, the same
+// of the high half and s.y, exact.  A nibble is spliced into the mantissa of
+// 1024 + c (at bit 0) or 64 + c (at bit 4); one fused operation takes off
+// the offset and applies the scale.
+__device__ __forceinline__ void widen(uint32_t w, const Scale2 &k, uint32_t (&p)[4]) {
     const uint32_t w8 = w >> 8;
-    p[0] = h2u(__hmul2(__hadd2(u2h(and_or(w, 0x000F000Fu, 0x64006400u)), m1032), s));
-    p[1] = h2u(__hfma2(u2h(and_or(w, 0x00F000F0u, 0x54005400u)), s, m72s));
-    p[2] = h2u(__hmul2(__hadd2(u2h(and_or(w8, 0x000F000Fu, 0x64006400u)), m1032), s));
-    p[3] = h2u(__hfma2(u2h(and_or(w8, 0x00F000F0u, 0x54005400u)), s, m72s));
+    p[0] = h2u(__hfma2(u2h(and_or(w, 0x000F000Fu, 0x64006400u)), k.s, k.m1032));
+    p[1] = h2u(__hfma2(u2h(and_or(w, 0x00F000F0u, 0x54005400u)), k.s, k.m72));
+    p[2] = h2u(__hfma2(u2h(and_or(w8, 0x000F000Fu, 0x64006400u)), k.s, k.m1032));
+    p[3] = h2u(__hfma2(u2h(and_or(w8, 0x00F000F0u, 0x54005400u)), k.s, k.m72));
 }
 
 __device__ __forceinline__ float exp2_fast(float x) {

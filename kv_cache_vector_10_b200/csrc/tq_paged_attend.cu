@@ -36,29 +36,36 @@ namespace {
 
 using namespace tqpaged;
 
-constexpr int NW = 4;                  // warps of a CTA
-constexpr int THREADS = 32 * NW;
+constexpr int NW = 4;                  // warps of a CTA that compute; one more requests the codes
+constexpr int THREADS = 32 * (NW + 1);
 
-template <int D>
+template <int D, int NT>
 struct Cfg {
     static constexpr int TT = D == 256 ? 32 : 64;              // tokens of a tile
-    static constexpr int NST = D == 64 ? 3 : 2;                // stages of a warp
-    static constexpr int CTAS = D == 64 ? 4 : 3;               // CTAs of an SM
-    using Load = TileLoad<D, TT>;
-    static constexpr int CODES = Load::CODES, SCALES = Load::SCALES, STAGE = Load::STAGE;
-    static constexpr int SMEM = NW * NST * STAGE;
+    static constexpr int NST = D == 64 ? 3 : 2;                // stages: a tile for each warp
+    // CTAs of an SM: as many as the registers of the larger fragments allow
+    static constexpr int CTAS = (D == 64 ? 4 : D == 128 ? 3 : 2) - (NT == 2 ? 1 : 0);
+    using Load = TileLoad<D, TT, NW>;
+    static constexpr int SMEM = NST * Load::STAGE;
 };
 
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+__device__ __forceinline__ void mma_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+                 : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     uint32_t y;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
 
@@ -119,7 +126,7 @@ __device__ __forceinline__ void load_queries(const PagedAttn &P, const Seq &s, i
             q[nt][4 * i + 3] = __byte_perm(w[i].y, w[i].w, 0x7632);
         }
 #pragma unroll
-        for (int c = 0; c < 2; ++c) mul[nt][c] = __shfl_sync(0xffffffffu, back, (2 * t + c) * 4) * P.scale_log2;
+        for (int c = 0; c < 2; ++c) mul[nt][c] = __shfl_sync(0xffffffffu, back, (2 * t + c) * 4) * (P.scale_log2 * WIDE);
     }
 }
 
@@ -128,57 +135,67 @@ __device__ __forceinline__ void store_out4(const PagedAttn &P, int64_t at, float
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(THREADS, Cfg<D>::CTAS) tq_paged_decode_kernel(const __grid_constant__ PagedAttn P) {
-    using C = Cfg<D>;
+__global__ void __launch_bounds__(THREADS, Cfg<D, NT>::CTAS) tq_paged_decode_kernel(const __grid_constant__ PagedAttn P) {
+    using C = Cfg<D, NT>;
     constexpr int TT = C::TT, NST = C::NST, R = 8 * NT, KW = D / 32, VW = D / 64, SUB = TT / 16;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ __align__(8) uint64_t bars[NW][NST];
-    __shared__ float s_m[NW][R], s_l[NW][R];
+    __shared__ __align__(8) uint64_t full[NST], freed[NST];
+    __shared__ uint32_t s_valid[NST];
+    __shared__ float s_m[2][NW][R], s_l[2][NW][R];   // by the item's parity: a warp may be one item ahead
     __shared__ Share s_share;
-    __shared__ long long s_sum[NW];
+    __shared__ long long s_sum[NW + 1];
     __shared__ int s_abort;
+    static_assert(NW * R * D * 4 <= C::Load::STAGE, "a stage holds the warps' parts of an item");
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     if (tid == 0) {
         s_abort = tqdev::status_aborted(P.status) ? 1 : 0;
-        for (int w = 0; w < NW; ++w)
-            for (int i = 0; i < NST; ++i) tqdev::mbar_init(&bars[w][i], 1);
+        for (int i = 0; i < NST; ++i) {
+            tqdev::mbar_init(&full[i], 1);
+            tqdev::mbar_init(&freed[i], NW);
+        }
         tqdev::fence_barrier_init();
     }
     tqdev::grid_dep_trigger();
     const Share sh = find_share<R, TT, THREADS>(P, &s_share, s_sum);
-    if (tid == 0) P.rec[blockIdx.x] = make_int4(-1, 0, 0, 0);
-    if (s_abort || sh.lo >= sh.hi) return;
-
-    uint8_t *ring = smem + warp * (NST * C::STAGE);
-    uint64_t *bar = bars[warp];
-    int used = 0, filled = 0;         // tiles of this warp consumed and requested, over all items
-    uint32_t valid_pages = 0;         // four bits a stage: which parts of the tile were copied
+    if (s_abort || sh.lo >= sh.hi) {
+        if (tid == 0) static_cast<Joint *>(P.rec)[blockIdx.x].rows = 0;
+        return;
+    }
     bool failed = false;
-
     Walk<R, TT> it;
-    for (it.begin(P, sh); it.more(); it.next(P)) {
+    it.begin(P, sh);
+    if (warp == NW) {
+        // --------------------------------------------- requests, items ahead
+        if (lane == 0) static_cast<Joint *>(P.rec)[blockIdx.x] = it.joint(sh);
+        const typename C::Load load(P, lane);
+        int n = 0;
+        for (; it.more() && !failed; it.next(P)) {
+            int tok = load.token(it.tl, it.i0, it.i1, it.s.len), page = C::Load::fetch(P, it.b, tok);
+            for (int i = it.i0; i < it.i1; i += NW, ++n) {
+                const int st = n % NST, tok2 = load.token(it.tl, i + NW, it.i1, it.s.len), page2 = C::Load::fetch(P, it.b, tok2);
+                if (n >= NST && !__all_sync(0xffffffffu, tqdev::mbar_wait_bounded(&freed[st], (uint32_t)(n / NST - 1) & 1u))) {
+                    failed = true;
+                    break;
+                }
+                load.request(P, tok, page, it.h, lane, smem + st * C::Load::STAGE, &s_valid[st], &full[st]);
+                tok = tok2;
+                page = page2;
+            }
+        }
+        // whatever became of the others: the copies in flight have landed
+        for (int k = max(0, n - NST); k < n; ++k) failed |= !tqdev::mbar_wait_bounded(&full[k % NST], (uint32_t)(k / NST) & 1u);
+        if (failed) atomicOr(reinterpret_cast<unsigned int *>(P.status + 1), TQ_FLAG_WAIT_TIMEOUT);
+        return;
+    }
+
+    int n = 0;                        // stages consumed, over all items
+    for (int items = 0; it.more(); it.next(P), ++items) {
         const Seq &s = it.s;
         const Tiles &tl = it.tl;
-        const int i0 = it.i0, i1 = it.i1, lg_part = C::Load::lg_part(P), parts = TT >> lg_part;
-        // page numbers are fetched one tile ahead of their use
-        auto fetch = [&](int i) { return i < i1 ? C::Load::fetch(P, it.b, s.len, tile_token(tl, i, TT), lane) : -1; };
-        int next_page = fetch(i0 + warp);
-        auto request = [&](int i) {
-            const int st = filled % NST, page = next_page;
-            next_page = fetch(i + NW);
-            const uint32_t got = C::Load::request(P, page, it.h, s.len, tile_token(tl, i, TT), lane, ring + st * C::STAGE, &bar[st]);
-            valid_pages = (valid_pages & ~(15u << (4 * st))) | (got << (4 * st));
-            ++filled;
-        };
-
-        int ahead = i0 + warp;
-        for (int k = 0; k < NST; ++k, ahead += NW)
-            if (ahead < i1 && !failed) request(ahead);
-
+        const int lg_part = min(P.lg_page, TT == 64 ? 6 : 5), parts = TT >> lg_part;
         uint32_t q[NT][D / 8];
         float mul[NT][2], m_run[NT][2], l_run[NT][2], o[NT][D / 16][4];
-        int pos[NT][2];               // position of the query of column 2 t + c
         load_queries<D, NT>(P, s, it.h, it.row0, it.row1, lane, q, mul);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -186,7 +203,6 @@ __global__ void __launch_bounds__(THREADS, Cfg<D>::CTAS) tq_paged_decode_kernel(
             for (int c = 0; c < 2; ++c) {
                 m_run[nt][c] = -INFINITY;
                 l_run[nt][c] = 0.f;
-                pos[nt][c] = s.len - s.n + (it.row0 + 8 * nt + 2 * t + c) / P.G;
             }
 #pragma unroll
             for (int j = 0; j < D / 16; ++j)
@@ -194,17 +210,21 @@ __global__ void __launch_bounds__(THREADS, Cfg<D>::CTAS) tq_paged_decode_kernel(
                 for (int e = 0; e < 4; ++e) o[nt][j][e] = 0.f;
         }
 
-        for (int i = i0 + warp; i < i1 && !failed; i += NW) {
-            const int st = used % NST;
-            if (!__all_sync(0xffffffffu, tqdev::mbar_wait_bounded(&bar[st], (uint32_t)(used / NST) & 1u))) {
-                failed = true;
-                break;
+        uint8_t *stage = smem;
+        for (int i = it.i0; i < it.i1; i += NW, ++n) {
+            const int st = n % NST;
+            stage = smem + st * C::Load::STAGE;
+            if (n > 0 && i > it.i0) {   // the stage before may be filled again (an item's last: after the join below)
+                __syncwarp();
+                if (lane == 0) tqdev::mbar_arrive(&freed[(n - 1) % NST]);
             }
-            const uint8_t *kc = ring + st * C::STAGE, *vc = kc + C::CODES, *ks = vc + C::CODES, *vs = ks + C::SCALES;
-            const int T0 = tile_token(tl, i, TT);
-            const uint32_t got = valid_pages >> (4 * st);
-            const bool whole = T0 + TT - 1 <= tl.p_lo && (P.window <= 0 || T0 > tl.p_hi - P.window || T0 + TT <= P.sinks) &&
-                               (got & ((1u << parts) - 1u)) == (1u << parts) - 1u;
+            failed = failed || !__all_sync(0xffffffffu, tqdev::mbar_wait_bounded(&full[st], (uint32_t)(n / NST) & 1u));
+            if (failed || i + warp >= it.i1) continue;
+            const uint8_t *keys = stage + warp * C::Load::TILE, *vals = keys + C::Load::SIDE;
+            const int T0 = tile_token(tl, i + warp, TT);
+            const uint32_t all = (1u << parts) - 1u;
+            const uint32_t got = (*reinterpret_cast<volatile uint32_t *>(&s_valid[st]) >> (warp * parts)) & all;
+            const bool whole = T0 + TT - 1 <= tl.p_lo && (P.window <= 0 || T0 > tl.p_hi - P.window || T0 + TT <= P.sinks) && got == all;
 
             // scores: 16 tokens a step; rows g and g + 8 of the fragment are
             // the tokens (g / 2) + 4 (g % 2) and that + 8, so that the
@@ -214,28 +234,25 @@ __global__ void __launch_bounds__(THREADS, Cfg<D>::CTAS) tq_paged_decode_kernel(
 #pragma unroll
             for (int u = 0; u < SUB; ++u) {
                 uint32_t w0[KW], w1[KW];
-                const int ra = 16 * u + tok0, rb = ra + 8;
+                const uint8_t *kc = keys + C::Load::codes_at(16 * u, lg_part), *ks = keys + C::Load::scales_at(16 * u, lg_part);
+                const int ra = tok0, rb = tok0 + 8;
                 load_words<KW>(kc + ra * (D / 2) + t * (D / 8), w0);
                 load_words<KW>(kc + rb * (D / 2) + t * (D / 8), w1);
+                constexpr int GW = D == 256 ? 4 : KW;   // words of a lane in one group
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) sc[nt][u][e] = 0.f;
-#pragma unroll
-                for (int x = 0; x < KW; x += (D == 256 ? 4 : KW)) {   // the words of one group
+                for (int x = 0; x < KW; x += GW) {
                     const int grp = D == 64 ? t >> 1 : D == 128 ? t : 2 * t + x / 4;
-                    const __half2 s0 = u2h(ks[ra * (D / 32) + grp] * 0x00800080u);
-                    const __half2 s1 = u2h(ks[rb * (D / 32) + grp] * 0x00800080u);
-                    const __half2 m72 = __half2half2(__ushort_as_half(H_M72));   // -72
-                    const __half2 b0 = __hmul2(s0, m72), b1 = __hmul2(s1, m72);
+                    const Scale2 s0 = scale2(ks[ra * (D / 32) + grp] * 0x00010001u);
+                    const Scale2 s1 = scale2(ks[rb * (D / 32) + grp] * 0x00010001u);
 #pragma unroll
-                    for (int y = x; y < x + (D == 256 ? 4 : KW); ++y) {
+                    for (int y = x; y < x + GW; ++y) {
                         uint32_t a[4], c[4];
-                        widen(w0[y], s0, b0, a);
-                        widen(w1[y], s1, b1, c);
+                        widen(w0[y], s0, a);
+                        widen(w1[y], s1, c);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
-                            mma(sc[nt][u], a[0], c[0], a[1], c[1], q[nt][4 * y], q[nt][4 * y + 1]);
+                            if (y == 0) mma_first(sc[nt][u], a[0], c[0], a[1], c[1], q[nt][0], q[nt][1]);
+                            else mma(sc[nt][u], a[0], c[0], a[1], c[1], q[nt][4 * y], q[nt][4 * y + 1]);
                             mma(sc[nt][u], a[2], c[2], a[3], c[3], q[nt][4 * y + 2], q[nt][4 * y + 3]);
                         }
                     }
@@ -250,7 +267,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<D>::CTAS) tq_paged_decode_kernel(
                         const int tok = T0 + 16 * u + tok0 + (e >= 2 ? 8 : 0);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
-                            const int p = pos[nt][e & 1];
+                            const int p = s.len - s.n + (it.row0 + 8 * nt + 2 * t + (e & 1)) / P.G;
                             const bool see = have && tok <= p && (P.window <= 0 || tok > p - P.window || tok < P.sinks);
                             if (!see) sc[nt][u][e] = -INFINITY;
                         }
@@ -309,26 +326,25 @@ __global__ void __launch_bounds__(THREADS, Cfg<D>::CTAS) tq_paged_decode_kernel(
             // tokens t, t + 4, t + 8, t + 12 of each sixteen
 #pragma unroll
             for (int u = 0; u < SUB; ++u) {
+                const uint8_t *vc = vals + C::Load::codes_at(16 * u, lg_part), *vs = vals + C::Load::scales_at(16 * u, lg_part);
                 uint32_t w[4][VW], sv[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const int r = 16 * u + t + 4 * k;
+                    const int r = t + 4 * k;
                     load_words<VW>(vc + r * (D / 2) + g * (D / 16), w[k]);
                     sv[k] = vs[r * (D / 32) + (g * (D / 8)) / 32];
                     // rows that hold no token of this sequence may hold anything
-                    if (!whole && (T0 + r >= s.len || !((got >> ((16 * u) >> lg_part)) & 1u))) sv[k] = 0;
+                    if (!whole && (T0 + 16 * u + r >= s.len || !((got >> ((16 * u) >> lg_part)) & 1u))) sv[k] = 0;
                 }
-                const __half2 m72 = __half2half2(__ushort_as_half(H_M72));
-                const __half2 s0 = u2h(sv[0] * 0x80u + sv[1] * 0x800000u), s1 = u2h(sv[2] * 0x80u + sv[3] * 0x800000u);
-                const __half2 b0 = __hmul2(s0, m72), b1 = __hmul2(s1, m72);
+                const Scale2 s0 = scale2(sv[0] | sv[1] << 16), s1 = scale2(sv[2] | sv[3] << 16);
 #pragma unroll
                 for (int y = 0; y < VW; ++y) {
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
                         const uint32_t sel = half ? 0x7632u : 0x5410u;
                         uint32_t a[4], c[4];
-                        widen(__byte_perm(w[0][y], w[1][y], sel), s0, b0, a);
-                        widen(__byte_perm(w[2][y], w[3][y], sel), s1, b1, c);
+                        widen(__byte_perm(w[0][y], w[1][y], sel), s0, a);
+                        widen(__byte_perm(w[2][y], w[3][y], sel), s1, c);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
                             mma(o[nt][4 * y + 2 * half], a[0], a[1], c[0], c[1], pw[nt][u][0], pw[nt][u][1]);
@@ -337,15 +353,11 @@ __global__ void __launch_bounds__(THREADS, Cfg<D>::CTAS) tq_paged_decode_kernel(
                     }
                 }
             }
-            ++used;
-            __syncwarp();
-            if (ahead < i1) {
-                request(ahead);
-                ahead += NW;
-            }
         }
 
-        // the warps' parts of this item, joined through shared memory
+        // The warps' parts of this item, joined through the last stage used
+        // (the next one is being filled meanwhile).
+        float(*sm)[R] = s_m[items & 1], (*sl)[R] = s_l[items & 1];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -355,46 +367,44 @@ __global__ void __launch_bounds__(THREADS, Cfg<D>::CTAS) tq_paged_decode_kernel(
                 l += __shfl_xor_sync(0xffffffffu, l, 8);
                 l += __shfl_xor_sync(0xffffffffu, l, 16);
                 if (g == 0) {
-                    s_m[warp][8 * nt + 2 * t + c] = m_run[nt][c];
-                    s_l[warp][8 * nt + 2 * t + c] = l;
+                    sm[warp][8 * nt + 2 * t + c] = m_run[nt][c];
+                    sl[warp][8 * nt + 2 * t + c] = l;
                 }
             }
-        __syncthreads();
-        float *mine = reinterpret_cast<float *>(ring);
+        tqdev::named_sync(1, 32 * NW);
+        float *all_parts = reinterpret_cast<float *>(stage);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 const int r = 8 * nt + 2 * t + c;
-                float m = s_m[0][r];
+                float m = sm[0][r];
 #pragma unroll
-                for (int w = 1; w < NW; ++w) m = fmaxf(m, s_m[w][r]);
-                const float f = m_run[nt][c] == -INFINITY ? 0.f : exp2_fast(m_run[nt][c] - m);
-                if (!failed) {
+                for (int w = 1; w < NW; ++w) m = fmaxf(m, sm[w][r]);
+                const float f = m_run[nt][c] == -INFINITY ? 0.f : exp2_fast(m_run[nt][c] - m) * WIDE;
 #pragma unroll
-                    for (int j = 0; j < D / 16; ++j)
-                        *reinterpret_cast<float2 *>(mine + r * D + g * (D / 8) + 8 * (j >> 2) + 2 * (j & 3)) =
-                            make_float2(o[nt][j][c] * f, o[nt][j][c + 2] * f);
-                }
+                for (int j = 0; j < D / 16; ++j)
+                    *reinterpret_cast<float2 *>(all_parts + (warp * R + r) * D + g * (D / 8) + 8 * (j >> 2) + 2 * (j & 3)) =
+                        make_float2(o[nt][j][c] * f, o[nt][j][c + 2] * f);
             }
-        __syncthreads();
-        const bool begins = it.begins(), ends = it.ends();
-        float *part = P.part + ((int64_t)blockIdx.x * 2 + (begins ? 1 : 0)) * (R * (D + 2));
-        for (int x = tid; x < R * D / 4; x += THREADS) {
+        tqdev::named_sync(1, 32 * NW);
+        const bool direct = it.begins() && it.ends();
+        float *part = P.part + ((int64_t)blockIdx.x * 2 + (it.begins() ? 1 : 0)) * (R * (D + 2));
+        for (int x = tid; x < R * D / 4; x += 32 * NW) {
             const int r = x / (D / 4), c4 = x % (D / 4);
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int w = 0; w < NW; ++w) {
-                const float4 y = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(smem + w * (NST * C::STAGE)) + r * D + 4 * c4);
+                const float4 y = *reinterpret_cast<const float4 *>(all_parts + (w * R + r) * D + 4 * c4);
                 v.x += y.x, v.y += y.y, v.z += y.z, v.w += y.w;
             }
-            float m = s_m[0][r], l = 0.f;
+            float m = sm[0][r], l = 0.f;
 #pragma unroll
-            for (int w = 1; w < NW; ++w) m = fmaxf(m, s_m[w][r]);
+            for (int w = 1; w < NW; ++w) m = fmaxf(m, sm[w][r]);
 #pragma unroll
             for (int w = 0; w < NW; ++w)
-                if (s_m[w][r] != -INFINITY) l += s_l[w][r] * exp2_fast(s_m[w][r] - m);
-            if (begins && ends) {
+                if (sm[w][r] != -INFINITY) l += sl[w][r] * exp2_fast(sm[w][r] - m);
+            if (direct) {
                 if (it.row0 + r < it.row1) {
                     const float inv = l != 0.f ? 1.f / l : 0.f;
                     store_out4(P, out_at(P, s, it.h, it.row0 + r) + 4 * c4, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
@@ -407,80 +417,88 @@ __global__ void __launch_bounds__(THREADS, Cfg<D>::CTAS) tq_paged_decode_kernel(
                 }
             }
         }
-        if (begins && !ends && tid == 0) P.rec[blockIdx.x] = make_int4(it.b, it.h, it.row0, it.last_cta(sh));
         tqdev::fence_proxy_async_smem();
-        __syncthreads();
+        __syncwarp();
+        if (lane == 0) tqdev::mbar_arrive(&freed[(n - 1) % NST]);
     }
-    // a warp that gave up waits (again with a limit) for its copies in flight
-    if (failed) {
-        atomicOr(reinterpret_cast<unsigned int *>(P.status + 1), TQ_FLAG_WAIT_TIMEOUT);
-        for (; used < filled; ++used) tqdev::mbar_wait_bounded(&bar[used % NST], (uint32_t)(used / NST) & 1u);
-    }
+    if (failed) atomicOr(reinterpret_cast<unsigned int *>(P.status + 1), TQ_FLAG_WAIT_TIMEOUT);
 }
 
-// Joins the parts of the items that were cut between CTAs.  Block x looks
-// after the item that begins in CTA x and goes on in the next (at most one),
-// rows [8 y, 8 y + 8); the threads split the parts and add them in a fixed
-// order.
+// Joins the parts of the items that were cut between CTAs.  The blocks
+// (x, y) serve the item that CTA x took over from the one before; an item of
+// n parts has n - 1 such x, and all their warps share its groups of four
+// outputs.  A warp's lanes split a few of these and the parts, and add up in
+// a fixed order.
+constexpr int JOIN_WARPS = 4;
+
 template <int D>
-__global__ void __launch_bounds__(1024) tq_paged_join_kernel(const __grid_constant__ PagedAttn P, int R) {
-    constexpr int LANES = 8 * D / 4, GROUPS = 1024 / LANES;
-    __shared__ float4 s_o[GROUPS][LANES];
-    __shared__ float s_l[GROUPS][8];
+__global__ void __launch_bounds__(32 * JOIN_WARPS) tq_paged_join_kernel(const __grid_constant__ PagedAttn P, int R) {
     tqdev::grid_dep_wait();
-    if (tqdev::status_aborted(P.status)) return;
-    const int4 rec = P.rec[blockIdx.x];
-    if (rec.x < 0) return;
-    bool bad = false;
-    const Seq s = load_seq(P, rec.x, bad);
-    const int first = blockIdx.x, last = rec.w;
-    const int lane = threadIdx.x % LANES, grp = threadIdx.x / LANES;
-    const int r = blockIdx.y * 8 + lane / (D / 4), c4 = lane % (D / 4);
+    const Joint J = static_cast<const Joint *>(P.rec)[blockIdx.x];
+    if (tqdev::status_aborted(P.status) || J.rows <= 0) return;
+    const int lane = threadIdx.x & 31, slices = JOIN_WARPS * gridDim.y;
+    const int n = J.last - J.first + 1, warps = (n - 1) * slices;
+    const int me = (blockIdx.x - J.first - 1) * slices + blockIdx.y * JOIN_WARPS + (threadIdx.x >> 5);
+    const int total = J.rows * (D / 4), each = (total + warps - 1) / warps;
+    const int c0 = me * each, c1 = min(total, c0 + each);
+    const int lg = each > 1 ? 32 - __clz(min(each, 32) - 1) : 0, groups = 32 >> lg;   // columns at once (log2), parts at once
+    const int col = lane & ((1 << lg) - 1), grp = lane >> lg;
     const int64_t size = (int64_t)R * (D + 2);
-    auto part = [&](int c) { return P.part + ((int64_t)c * 2 + (c == first ? 1 : 0)) * size; };
-    float m = -INFINITY;
-    for (int c = first; c <= last; ++c) m = fmaxf(m, __ldcg(part(c) + R * D + r));
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    float l = 0.f;
-#pragma unroll 4
-    for (int c = first + grp; c <= last; c += GROUPS) {
-        const float *p = part(c);
-        const float mc = __ldcg(p + R * D + r);
-        const float f = mc == -INFINITY ? 0.f : exp2_fast(mc - m);
-        const float4 y = __ldcg(reinterpret_cast<const float4 *>(p + r * D) + c4);
-        v.x += y.x * f, v.y += y.y * f, v.z += y.z * f, v.w += y.w * f;
-        l += __ldcg(p + R * D + R + r) * f;
-    }
-    s_o[grp][lane] = v;
-    if (c4 == 0) s_l[grp][lane / (D / 4)] = l;
-    __syncthreads();
-    if (grp) return;
-    l = 0.f;
+    const Seq s{(int)J.q0, 0, 0};
+    for (int c = c0; c < c1; c += 1 << lg) {
+        const int x = min(c + col, c1 - 1), r = x / (D / 4), c4 = x % (D / 4);
+        float m = -INFINITY, l = 0.f;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        auto add = [&](float mk, float lk, const float4 &y) {
+            if (mk == -INFINITY) return;
+            const float to = fmaxf(m, mk), f = m == -INFINITY ? 0.f : exp2_fast(m - to), g = exp2_fast(mk - to);
+            m = to;
+            l = l * f + lk * g;
+            v.x = v.x * f + y.x * g, v.y = v.y * f + y.y * g, v.z = v.z * f + y.z * g, v.w = v.w * f + y.w * g;
+        };
+        constexpr int B = 4;   // parts on their way at once
+        for (int k0 = grp; k0 < n; k0 += B * groups) {
+            float mk[B], lk[B];
+            float4 y[B];
 #pragma unroll
-    for (int k = 0; k < GROUPS; ++k) l += s_l[k][lane / (D / 4)];
+            for (int b = 0; b < B; ++b) {
+                const int k = k0 + b * groups;
+                mk[b] = -INFINITY;
+                if (k < n) {
+                    const float *p = P.part + ((int64_t)(J.first + k) * 2 + (k == 0 ? 1 : 0)) * size;
+                    mk[b] = __ldcg(p + (int64_t)R * D + r);
+                    lk[b] = __ldcg(p + (int64_t)R * D + R + r);
+                    y[b] = __ldcg(reinterpret_cast<const float4 *>(p + (int64_t)r * D) + c4);
+                }
+            }
 #pragma unroll
-    for (int k = 1; k < GROUPS; ++k) {
-        const float4 y = s_o[k][lane];
-        v.x += y.x, v.y += y.y, v.z += y.z, v.w += y.w;
+            for (int b = 0; b < B; ++b) add(mk[b], lk[b], y[b]);
+        }
+        for (int o = 16; o >= (1 << lg); o >>= 1) {
+            const float mo = __shfl_xor_sync(0xffffffffu, m, o), lo = __shfl_xor_sync(0xffffffffu, l, o);
+            const float4 z = make_float4(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o),
+                                         __shfl_xor_sync(0xffffffffu, v.z, o), __shfl_xor_sync(0xffffffffu, v.w, o));
+            add(mo, lo, z);
+        }
+        if (grp == 0 && c + col < c1) {
+            const float inv = l != 0.f ? 1.f / l : 0.f;
+            store_out4(P, out_at(P, s, (int)J.h, J.row0 + r) + 4 * c4, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+        }
     }
-    const int row = rec.z + r;
-    if (row >= s.n * P.G) return;
-    const float inv = l != 0.f ? 1.f / l : 0.f;
-    store_out4(P, out_at(P, s, rec.y, row) + 4 * c4, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
 }
 
 template <int D, int NT>
 tq_status launch_decode(PagedAttn P, int64_t tiles_bound, int n_sms, cudaStream_t stream, size_t *need) {
-    using C = Cfg<D>;
+    using C = Cfg<D, NT>;
     constexpr int R = 8 * NT;
     P.min_tiles = NW;
     const int grid = (int)std::max<int64_t>(1, std::min<int64_t>((int64_t)n_sms * C::CTAS, (tiles_bound + NW - 1) / NW));
-    const size_t rec_bytes = ((size_t)grid * sizeof(int4) + 255) / 256 * 256;
+    const size_t rec_bytes = ((size_t)grid * sizeof(Joint) + 255) / 256 * 256;
     if (need) {
         *need = rec_bytes + (size_t)grid * 2 * R * (D + 2) * sizeof(float);
         return TQ_OK;
     }
-    P.rec = reinterpret_cast<int4 *>(P.part);
+    P.rec = P.part;
     P.part = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(P.part) + rec_bytes);
     cudaError_t e = cudaFuncSetAttribute(tq_paged_decode_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e == cudaSuccess) {
@@ -495,7 +513,7 @@ template <int D>
 tq_status launch_dim(const PagedAttn &P, int max_q_len, int n_sms, cudaStream_t stream, size_t *need) {
     const int64_t rows = (int64_t)max_q_len * P.G;
     const int nt = (rows <= 8 || D == 256) ? 1 : 2;
-    const int64_t tiles = (int64_t)P.batch * P.Hkv * ((rows + 8 * nt - 1) / (8 * nt)) * (P.max_tokens / Cfg<D>::TT + 1);
+    const int64_t tiles = (int64_t)P.batch * P.Hkv * ((rows + 8 * nt - 1) / (8 * nt)) * (P.max_tokens / Cfg<D, 1>::TT + 1);
     if constexpr (D != 256)
         if (nt == 2) return launch_decode<D, 2>(P, tiles, n_sms, stream, need);
     return launch_decode<D, 1>(P, tiles, n_sms, stream, need);
@@ -505,7 +523,7 @@ tq_status launch_dim(const PagedAttn &P, int max_q_len, int n_sms, cudaStream_t 
 
 tq_status tq_launch_paged_join(int d, const PagedAttn &P, int grid, int rows, cudaStream_t stream) {
     const auto kern = d == 64 ? tq_paged_join_kernel<64> : d == 128 ? tq_paged_join_kernel<128> : tq_paged_join_kernel<256>;
-    return tq_check_cuda(tq_launch_dependent(kern, dim3(grid, rows / 8), dim3(1024), 0, stream, P, rows));
+    return tq_check_cuda(tq_launch_dependent(kern, dim3(grid, std::max(1, rows / 32)), dim3(32 * JOIN_WARPS), 0, stream, P, rows));
 }
 
 tq_status tq_launch_paged_attention(const tq_paged *ctx, const PagedAttn &P, int max_q_len, int n_sms,

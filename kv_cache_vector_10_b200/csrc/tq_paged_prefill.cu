@@ -33,7 +33,7 @@ struct Pre {
     static constexpr int R = 128 * NM;
     static constexpr int NB = D == 256 ? 2 : 3;      // widened tiles in shared memory
     static constexpr int NC = 3;                     // code tiles in shared memory
-    using Load = TileLoad<D, PT>;
+    using Load = TileLoad<D, PT, 1>;
     static constexpr int KX = PT * 128;              // 64 channels of a tile: rows of 128 bytes, swizzled
     static constexpr int TILE = (D / 64) * KX;
     static constexpr int OFF_V = NB * TILE, OFF_C = 2 * NB * TILE;
@@ -124,20 +124,24 @@ __global__ void __launch_bounds__(Pre<D, NM>::THREADS, 1) tq_paged_prefill_kerne
         }
         tqdev::mbar_init(&bars.done, 1);
         s_abort = tqdev::status_aborted(P.status) ? 1 : 0;
-        P.rec[blockIdx.x] = make_int4(-1, 0, 0, 0);
         tqdev::fence_barrier_init();
     }
     const Share sh = find_share<R, PT, C::THREADS>(P, &s_share, s_sum);
-    if (s_abort || sh.lo >= sh.hi) return;
+    if (s_abort || sh.lo >= sh.hi) {
+        if (tid == 0) static_cast<Joint *>(P.rec)[blockIdx.x].rows = 0;
+        return;
+    }
     if (warp == 0) tqdev::tmem_alloc(&s_tmem, 512);
     tqdev::tc_fence_before();
     __syncthreads();
     tqdev::tc_fence_after();
     const uint32_t tmem = s_tmem;
-    const int lg_part = C::Load::lg_part(P), parts = PT >> lg_part;
+    const int lg_part = min(P.lg_page, 6), parts = PT >> lg_part;
     const uint32_t all_parts = (1u << parts) - 1u;
     bool failed = false;
     Walk<R, PT> it;
+    it.begin(P, sh);
+    if (tid == 0) static_cast<Joint *>(P.rec)[blockIdx.x] = it.joint(sh);
 
     if (warp < SW) {
         // ------------------------------------------------------------- softmax
@@ -145,7 +149,7 @@ __global__ void __launch_bounds__(Pre<D, NM>::THREADS, 1) tq_paged_prefill_kerne
         const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
         const uint32_t t_o = lanes + m * D, t_q = lanes + C::COL_Q + m * (D / 2);
         int n = 0;
-        for (it.begin(P, sh); it.more() && !failed; it.next(P)) {
+        for (; it.more() && !failed; it.next(P)) {
             const Seq &s = it.s;
             const int row = it.row0 + r;
             const bool active = row < it.row1;
@@ -163,7 +167,7 @@ __global__ void __launch_bounds__(Pre<D, NM>::THREADS, 1) tq_paged_prefill_kerne
                 for (int i = 0; i < D / 8; ++i) a = __vmaxu2(a, amax4(__ldg(src + i)));
                 query_factor(max(a >> 16, a & 0xFFFFu), up, mul);
             }
-            mul *= P.scale_log2;
+            mul *= P.scale_log2 * WIDE;
 #pragma unroll
             for (int c = 0; c < D / 64; ++c) {
                 float x[32];
@@ -259,7 +263,7 @@ __global__ void __launch_bounds__(Pre<D, NM>::THREADS, 1) tq_paged_prefill_kerne
             }
             tqdev::tc_fence_after();
             const bool direct = it.begins() && it.ends();
-            const float inv = !direct ? 1.f : l_run != 0.f ? 1.f / l_run : 0.f;
+            const float inv = !direct ? WIDE : l_run != 0.f ? WIDE / l_run : 0.f;
             uint16_t *out = static_cast<uint16_t *>(P.out) + (active ? out_at(P, s, it.h, row) : 0);
             float *part = P.part + ((int64_t)blockIdx.x * 2 + (it.begins() ? 1 : 0)) * (R * (D + 2));
 #pragma unroll 1
@@ -282,7 +286,6 @@ __global__ void __launch_bounds__(Pre<D, NM>::THREADS, 1) tq_paged_prefill_kerne
             if (!direct) {
                 part[R * D + r] = m_run;
                 part[R * D + R + r] = l_run;
-                if (it.begins() && tid == 0) P.rec[blockIdx.x] = make_int4(it.b, it.h, it.row0, it.last_cta(sh));
             }
             tqdev::tc_fence_before();
         }
@@ -294,8 +297,9 @@ __global__ void __launch_bounds__(Pre<D, NM>::THREADS, 1) tq_paged_prefill_kerne
         // their chunks fall into different banks.
         const int e = warp - SW;
         const int sub = lane & 1, tr = 16 * e + (lane >> 1);   // token row of this lane, every tile
+        const int codes_at = C::Load::codes_at(tr, lg_part), scales_at = C::Load::scales_at(tr, lg_part);
         int n = 0;
-        for (it.begin(P, sh); it.more() && !failed; it.next(P)) {
+        for (; it.more() && !failed; it.next(P)) {
             for (int i = it.i0; i < it.i1; ++i, ++n) {
                 const int cs = n % NC, b = n % NB;
                 if (!wait_warp(&bars.codes_full[cs], (uint32_t)(n / NC) & 1u)) {
@@ -303,7 +307,6 @@ __global__ void __launch_bounds__(Pre<D, NM>::THREADS, 1) tq_paged_prefill_kerne
                     break;
                 }
                 const uint8_t *codes = sm + C::OFF_C + cs * C::Load::STAGE;
-                const uint8_t *scales = codes + 2 * C::Load::CODES;
                 const uint32_t got = *reinterpret_cast<volatile uint32_t *>(&s_valid[n & 15]);
                 // a row that holds no token of this sequence may hold anything
                 const bool there = tile_token(it.tl, i, PT) + tr < it.s.len && ((got >> (tr >> lg_part)) & 1u);
@@ -317,15 +320,14 @@ __global__ void __launch_bounds__(Pre<D, NM>::THREADS, 1) tq_paged_prefill_kerne
 #pragma unroll
                     for (int blk = 0; blk < D / 64; ++blk) {
                         const int grp = 2 * blk + sub;
-                        const uint4 w = *reinterpret_cast<const uint4 *>(codes + kv * C::Load::CODES + tr * (D / 2) + grp * 16);
-                        const uint32_t sb = there ? scales[kv * C::Load::SCALES + tr * (D / 32) + grp] : 0u;
-                        const __half2 sc = u2h(sb * 0x00800080u);
-                        const __half2 m72s = __hmul2(sc, __half2half2(__ushort_as_half(H_M72)));
+                        const uint4 w = *reinterpret_cast<const uint4 *>(codes + kv * C::Load::SIDE + codes_at + grp * 16);
+                        const uint32_t sb = there ? codes[kv * C::Load::SIDE + scales_at + grp] : 0u;
+                        const Scale2 sc = scale2(sb * 0x00010001u);
                         const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             uint32_t p[4];
-                            widen(ws[j], sc, m72s, p);
+                            widen(ws[j], sc, p);
                             *reinterpret_cast<uint4 *>(dst + blk * C::KX + (((4 * sub + j) ^ (tr & 7)) << 4)) =
                                 make_uint4(p[0], p[1], p[2], p[3]);
                         }
@@ -340,24 +342,19 @@ __global__ void __launch_bounds__(Pre<D, NM>::THREADS, 1) tq_paged_prefill_kerne
         }
     } else if (warp == SW + WIDEN_WARPS) {
         // ------------------------------------------------- requests of the codes
+        const typename C::Load load(P, lane);
         int n = 0;
-        for (it.begin(P, sh); it.more() && !failed; it.next(P)) {
-            int page = C::Load::fetch(P, it.b, it.s.len, tile_token(it.tl, it.i0, PT), lane);
+        for (; it.more() && !failed; it.next(P)) {
+            int tok = load.token(it.tl, it.i0, it.i1, it.s.len), page = C::Load::fetch(P, it.b, tok);
             for (int i = it.i0; i < it.i1; ++i, ++n) {
-                const int cs = n % NC;
-                const int next = i + 1 < it.i1 ? C::Load::fetch(P, it.b, it.s.len, tile_token(it.tl, i + 1, PT), lane) : -1;
+                const int cs = n % NC, tok2 = load.token(it.tl, i + 1, it.i1, it.s.len), page2 = C::Load::fetch(P, it.b, tok2);
                 if (n >= NC && !wait_warp(&bars.codes_free[cs], (uint32_t)(n / NC - 1) & 1u)) {
                     failed = true;
                     break;
                 }
-                // the parts are known before the copies that announce them
-                const int tok = tile_token(it.tl, i, PT) + (lane << lg_part);
-                const uint32_t got = __ballot_sync(0xffffffffu, lane < parts && tok < it.s.len && page >= 0 && page < P.n_pages);
-                if (lane == 0) *reinterpret_cast<volatile uint32_t *>(&s_valid[n & 15]) = got;
-                __syncwarp();
-                C::Load::request(P, page, it.h, it.s.len, tile_token(it.tl, i, PT), lane, sm + C::OFF_C + cs * C::Load::STAGE,
-                                 &bars.codes_full[cs]);
-                page = next;
+                load.request(P, tok, page, it.h, lane, sm + C::OFF_C + cs * C::Load::STAGE, &s_valid[n & 15], &bars.codes_full[cs]);
+                tok = tok2;
+                page = page2;
             }
         }
         // whatever happened to the others: the copies in flight have landed
@@ -388,7 +385,7 @@ __global__ void __launch_bounds__(Pre<D, NM>::THREADS, 1) tq_paged_prefill_kerne
         };
         int n = 0, items = 0;
         bool ok = true;
-        for (it.begin(P, sh); it.more() && ok; it.next(P), ++items) {
+        for (; it.more() && ok; it.next(P), ++items) {
             const int nt = it.i1 - it.i0;
             for (int m = 0; m < NM && ok; ++m) ok = tqdev::mbar_wait_bounded(&bars.q_ready[m], (uint32_t)items & 1u);
             for (int j = 0; j < (NM == 2 ? 1 : 2) && j < nt && ok; ++j) {
@@ -432,12 +429,12 @@ tq_status launch_prefill(PagedAttn P, int64_t tiles_bound, int n_sms, cudaStream
     using C = Pre<D, NM>;
     P.min_tiles = 4;
     const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(n_sms, (tiles_bound + P.min_tiles - 1) / P.min_tiles));
-    const size_t rec_bytes = ((size_t)grid * sizeof(int4) + 255) / 256 * 256;
+    const size_t rec_bytes = ((size_t)grid * sizeof(Joint) + 255) / 256 * 256;
     if (need) {
         *need = rec_bytes + (size_t)grid * 2 * C::R * (D + 2) * sizeof(float);
         return TQ_OK;
     }
-    P.rec = reinterpret_cast<int4 *>(P.part);
+    P.rec = P.part;
     P.part = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(P.part) + rec_bytes);
     cudaError_t e = cudaFuncSetAttribute(tq_paged_prefill_kernel<D, NM>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e == cudaSuccess) {
