@@ -15,7 +15,6 @@ Names follow the C ABI (``tq_create``, ``tq_encode_kv``,
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 
@@ -476,7 +475,8 @@ class PagedCache:
     k, v: the pool, uint8 [n_pages, n_kv_heads, page bytes].  Token t of page
     p is slot p * page_size + t.  Calls run on the cache's device, on
     `stream` or else on that device's current stream; their tensors must be
-    on that device."""
+    on that device.  A call's host work is a few microseconds beside its
+    launches, so the checks below are written out rather than shared."""
 
     def __init__(self, n_pages: int, n_kv_heads: int, head_dim: int, page_size: int = 64, device="cuda"):
         import torch
@@ -484,9 +484,10 @@ class PagedCache:
         if n_pages <= 0 or n_kv_heads <= 0:
             raise TQError(7, "PagedCache")                   # TQ_ERR_EMPTY
         device = torch.device(device)
+        if device.type != "cuda":
+            raise TQError(12, "PagedCache")                  # TQ_ERR_DEVICE
         self.device = torch.device("cuda", torch.cuda.current_device() if device.index is None else device.index)
         self.n_pages, self.n_kv_heads, self.head_dim, self.page_size = n_pages, n_kv_heads, head_dim, page_size
-        self._codes = {torch.float32: TQ_F32, torch.float16: TQ_F16, torch.bfloat16: TQ_BF16}
         out = ctypes.c_void_p()
         with torch.cuda.device(self.device):
             _check(_lib.tq_paged_create(head_dim, page_size, ctypes.byref(out)), "tq_paged_create")
@@ -494,6 +495,14 @@ class PagedCache:
         self.page_bytes = _lib.tq_paged_page_bytes(self.ctx)
         self.k = torch.zeros(n_pages, n_kv_heads, self.page_bytes, dtype=torch.uint8, device=self.device)
         self.v = torch.zeros_like(self.k)
+        self._prepare()
+
+    def _prepare(self):
+        import torch
+        self._torch, self._index = torch, self.device.index
+        self._codes = {torch.float32: TQ_F32, torch.float16: TQ_F16, torch.bfloat16: TQ_BF16}
+        self._halves = {torch.float16: TQ_F16, torch.bfloat16: TQ_BF16}
+        self._need = {}                                      # workspace bytes by shape
 
     def close(self):
         if self.ctx:
@@ -509,26 +518,24 @@ class PagedCache:
     def struct(self) -> tq_pages:
         return tq_pages(self.k.data_ptr(), self.v.data_ptr(), self.n_pages, self.n_kv_heads, 0)
 
-    def _on(self, stream):
-        """Makes `stream` and the cache's device current, where they are not."""
-        import torch
+    def _here(self, stream) -> bool:
+        """Whether the cache's device is current and `stream` is its current one (None)."""
+        return stream is None and self._torch._C._cuda_getDevice() == self._index
+
+    def _elsewhere(self, stream, call, *args, **kw):
+        """`call` with the cache's device and `stream` made current."""
         if stream is None:
-            if torch.cuda.current_device() == self.device.index:
-                return contextlib.nullcontext()
-            return torch.cuda.device(self.device)
+            with self._torch.cuda.device(self.device):
+                return call(*args, **kw)
         if stream.device != self.device:
             raise TQError(12, "PagedCache")                  # TQ_ERR_DEVICE
-        return torch.cuda.stream(stream)
-
-    def _want(self, where: str, *tensors):
-        for t in tensors:
-            if t is not None and t.device != self.device:
-                raise TQError(12, where)                     # TQ_ERR_DEVICE
+        with self._torch.cuda.stream(stream):
+            return call(*args, **kw)
 
     def _rows(self, t):
         """Rows as the library takes them: contiguous channels, 16-byte aligned starts (else a copy)."""
         sx, sh, sd = t.stride()
-        if sd == 1 and not (sx | sh) * t.element_size() % 16 and t.data_ptr() % 16 == 0:
+        if sd == 1 and not (sx | sh) * t.element_size() % 16 and not t.data_ptr() % 16:
             return t
         return t.clone() if t.is_contiguous() else t.contiguous()
 
@@ -538,58 +545,74 @@ class PagedCache:
         [n_tokens]; a negative slot is padding; the others must differ).
         With `stored`, returns the values that the cache keeps for them, in
         the rows' type (None for a None)."""
-        import torch
-        ref = k if k is not None else v
+        if not self._here(stream):
+            return self._elsewhere(stream, self.write, k, v, slots, stored)
+        torch = self._torch
+        ref = v if k is None else k
         if ref is None:
             raise TQError(1, "PagedCache.write")             # TQ_ERR_NULL
-        n, code = ref.shape[0] if ref.dim() else 0, self._codes.get(ref.dtype)
-        for t in (k, v):
-            if t is not None and (t.dtype != ref.dtype or t.shape != (n, self.n_kv_heads, self.head_dim)):
-                raise TQError(8, "PagedCache.write")         # TQ_ERR_DIM_MISMATCH
-        if code is None or slots.dtype != torch.int64 or slots.shape != (n,):
-            raise TQError(8, "PagedCache.write")
-        self._want("PagedCache.write", k, v, slots)
-        with self._on(stream):
+        n, code, dev = len(slots) if slots.dim() else -1, self._codes.get(ref.dtype), self._index
+        shape = (n, self.n_kv_heads, self.head_dim)
+        if code is None or slots.dtype is not torch.int64 or slots.dim() != 1:
+            raise TQError(8, "PagedCache.write")             # TQ_ERR_DIM_MISMATCH
+        if slots.get_device() != dev:
+            raise TQError(12, "PagedCache.write")
+        if not slots.is_contiguous():
             slots = slots.contiguous()
-            ks = vs = None
-            pk = pv = pks = pvs = None
-            sk = sv = (0, 0, 0)
-            if k is not None:
-                k = self._rows(k)
-                pk, sk = k.data_ptr(), k.stride()
-                if stored:
-                    ks = torch.empty(k.shape, dtype=k.dtype, device=self.device)
-                    pks = ks.data_ptr()
-            if v is not None:
-                v = self._rows(v)
-                pv, sv = v.data_ptr(), v.stride()
-                if stored:
-                    vs = torch.empty(v.shape, dtype=v.dtype, device=self.device)
-                    pvs = vs.data_ptr()
-            c = self.struct()
-            _check(_lib.tq_paged_write(self.ctx, pk, pv, code, n, sk[0], sk[1], sv[0], sv[1], slots.data_ptr(),
-                                       ctypes.byref(c), pks, pvs, _stream()), "tq_paged_write")
+        pk = pv = ks = vs = pks = pvs = None
+        skt = skh = svt = svh = 0
+        if k is not None:
+            if k.shape != shape:
+                raise TQError(8, "PagedCache.write")
+            if k.get_device() != dev:
+                raise TQError(12, "PagedCache.write")
+            k = self._rows(k)
+            pk, (skt, skh, _) = k.data_ptr(), k.stride()
+            if stored:
+                ks = torch.empty_like(k, memory_format=torch.contiguous_format)
+                pks = ks.data_ptr()
+        if v is not None:
+            if v.shape != shape or v.dtype is not ref.dtype:
+                raise TQError(8, "PagedCache.write")
+            if v.get_device() != dev:
+                raise TQError(12, "PagedCache.write")
+            v = self._rows(v)
+            pv, (svt, svh, _) = v.data_ptr(), v.stride()
+            if stored:
+                vs = torch.empty_like(v, memory_format=torch.contiguous_format)
+                pvs = vs.data_ptr()
+        err = _lib.tq_paged_write(self.ctx, pk, pv, code, n, skt, skh, svt, svh, slots.data_ptr(), self.struct(),
+                                  pks, pvs, torch._C._cuda_getCurrentRawStream(dev))
+        if err:
+            raise TQError(err, "tq_paged_write")
         return (ks, vs) if stored else None
 
     def read(self, slots, dtype=None, keys: bool = True, values: bool = True, stream=None):
         """The rows at `slots` (int64 [n_tokens]) as (k, v), each [n_tokens,
         n_kv_heads, head_dim] in `dtype` (default bfloat16; None for one not
         asked for); a negative slot gives zeros."""
-        import torch
-        dtype = dtype or torch.bfloat16
-        code = self._codes.get(dtype)
-        if code is None or slots.dim() != 1 or slots.dtype != torch.int64:
+        if not self._here(stream):
+            return self._elsewhere(stream, self.read, slots, dtype, keys, values)
+        torch = self._torch
+        code = self._codes.get(dtype or torch.bfloat16)
+        if code is None or slots.dim() != 1 or slots.dtype is not torch.int64:
             raise TQError(8, "PagedCache.read")
-        self._want("PagedCache.read", slots)
-        with self._on(stream):
+        if slots.get_device() != self._index:
+            raise TQError(12, "PagedCache.read")
+        if not slots.is_contiguous():
             slots = slots.contiguous()
-            shape = (slots.shape[0], self.n_kv_heads, self.head_dim)
-            kh = torch.empty(shape, dtype=dtype, device=self.device) if keys else None
-            vh = torch.empty(shape, dtype=dtype, device=self.device) if values else None
-            c = self.struct()
-            _check(_lib.tq_paged_read(self.ctx, ctypes.byref(c), slots.data_ptr(), shape[0],
-                                      kh.data_ptr() if keys else None, vh.data_ptr() if values else None, code,
-                                      _stream()), "tq_paged_read")
+        n = len(slots)
+        kh = vh = pk = pv = None
+        if keys:
+            kh = slots.new_empty((n, self.n_kv_heads, self.head_dim), dtype=dtype or torch.bfloat16)
+            pk = kh.data_ptr()
+        if values:
+            vh = slots.new_empty((n, self.n_kv_heads, self.head_dim), dtype=dtype or torch.bfloat16)
+            pv = vh.data_ptr()
+        err = _lib.tq_paged_read(self.ctx, self.struct(), slots.data_ptr(), n, pk, pv, code,
+                                 torch._C._cuda_getCurrentRawStream(self._index))
+        if err:
+            raise TQError(err, "tq_paged_read")
         return kh, vh
 
     def workspace_bytes(self, n_q_heads: int, batch: int, max_pages: int, max_q_len: int = 1) -> int:
@@ -606,45 +629,70 @@ class PagedCache:
         window: 0, or how many tokens back a query sees besides the first
         `sinks`; scale: default 1/sqrt(head_dim).  Returns `out` (like q;
         rows of no sequence are not written)."""
-        import torch
-        i32 = torch.int32
-        if q.dim() != 3 or page_table.dim() != 2 or q.dtype == torch.float32 or q.dtype not in self._codes:
+        if not self._here(stream):
+            return self._elsewhere(stream, self.attention, q, page_table, seq_lens, q_starts, max_q_len, window, sinks,
+                                   scale, out, workspace)
+        torch, dev, i32 = self._torch, self._index, self._torch.int32
+        code = self._halves.get(q.dtype)
+        if code is None or q.dim() != 3 or page_table.dim() != 2 or q.shape[2] != self.head_dim:
             raise TQError(8, "PagedCache.attention")
-        (total, heads, d), (batch, pages) = q.shape, page_table.shape
-        if (d != self.head_dim or page_table.dtype != i32 or seq_lens.dtype != i32 or seq_lens.shape != (batch,) or
-                (q_starts is not None and (q_starts.dtype != i32 or q_starts.shape != (batch + 1,))) or
-                (out is not None and (out.shape != q.shape or out.dtype != q.dtype or out.stride(2) != 1))):
+        total, heads, _ = q.shape
+        batch, pages = page_table.shape
+        if page_table.dtype is not i32 or seq_lens.dtype is not i32 or seq_lens.shape != (batch,):
             raise TQError(8, "PagedCache.attention")
-        self._want("PagedCache.attention", q, page_table, seq_lens, q_starts, out, workspace)
+        if q.get_device() != dev or page_table.get_device() != dev or seq_lens.get_device() != dev:
+            raise TQError(12, "PagedCache.attention")
+        starts = None
+        if q_starts is not None:
+            if q_starts.dtype is not i32 or q_starts.shape != (batch + 1,):
+                raise TQError(8, "PagedCache.attention")
+            if q_starts.get_device() != dev:
+                raise TQError(12, "PagedCache.attention")
+            q_starts = q_starts.contiguous()
+            starts = q_starts.data_ptr()
         most = max_q_len or (1 if q_starts is None else max(total, 1))
-        with self._on(stream):
-            q, seq_lens = self._rows(q), seq_lens.contiguous()
-            if page_table.stride(1) != 1 or page_table.stride(0) < pages:
-                page_table = page_table.contiguous()
-            if q_starts is not None:
-                q_starts = q_starts.contiguous()
-            if out is None:
-                out = torch.empty(total, heads, d, dtype=q.dtype, device=self.device)
-            if workspace is None:
-                need = self.workspace_bytes(heads, batch, pages, most)
-                workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
-            (sqt, sqh, _), (sot, soh, _) = q.stride(), out.stride()
-            c = self.struct()
-            _check(_lib.tq_paged_attention(
-                self.ctx, ctypes.byref(c), q.data_ptr(), self._codes[q.dtype], total, heads, sqt, sqh,
-                page_table.data_ptr(), max(page_table.stride(0), pages), pages, seq_lens.data_ptr(),
-                None if q_starts is None else q_starts.data_ptr(), batch, most, window, sinks, scale or 0.0,
-                out.data_ptr(), sot, soh, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                _stream()), "tq_paged_attention")
+        q, seq_lens = self._rows(q), seq_lens.contiguous()
+        srow, scol = page_table.stride()
+        if scol != 1 or srow < pages:
+            page_table = page_table.contiguous()
+            srow = pages
+        if out is None:
+            out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        elif out.shape != q.shape or out.dtype is not q.dtype or out.stride(2) != 1:
+            raise TQError(8, "PagedCache.attention")
+        elif out.get_device() != dev:
+            raise TQError(12, "PagedCache.attention")
+        if workspace is None:
+            key = (heads, batch, pages, most)
+            need = self._need.get(key)
+            if need is None:
+                if len(self._need) > 4096:
+                    self._need.clear()
+                need = self._need[key] = self.workspace_bytes(*key)
+            workspace = q.new_empty(need, dtype=torch.uint8)
+        elif workspace.get_device() != dev:
+            raise TQError(12, "PagedCache.attention")
+        else:
+            need = workspace.numel() * workspace.element_size()
+        sqt, sqh, _ = q.stride()
+        sot, soh, _ = out.stride()
+        err = _lib.tq_paged_attention(
+            self.ctx, self.struct(), q.data_ptr(), code, total, heads, sqt, sqh, page_table.data_ptr(), srow, pages,
+            seq_lens.data_ptr(), starts, batch, most, window, sinks, scale or 0.0, out.data_ptr(), sot, soh,
+            workspace.data_ptr(), need, torch._C._cuda_getCurrentRawStream(dev))
+        if err:
+            raise TQError(err, "tq_paged_attention")
         return out
 
     def status(self, stream=None):
         """(rows not finite so far, error flags); synchronises the stream."""
+        if not self._here(stream):
+            return self._elsewhere(stream, self.status)
         n, f = ctypes.c_uint64(), ctypes.c_uint32()
-        with self._on(stream):
-            _check(_lib.tq_paged_get_status(self.ctx, _stream(), ctypes.byref(n), ctypes.byref(f)), "tq_paged_get_status")
+        _check(_lib.tq_paged_get_status(self.ctx, _stream(), ctypes.byref(n), ctypes.byref(f)), "tq_paged_get_status")
         return n.value, f.value
 
     def reset_status(self, stream=None):
-        with self._on(stream):
-            _check(_lib.tq_paged_reset_status(self.ctx, _stream()), "tq_paged_reset_status")
+        if not self._here(stream):
+            return self._elsewhere(stream, self.reset_status)
+        _check(_lib.tq_paged_reset_status(self.ctx, _stream()), "tq_paged_reset_status")

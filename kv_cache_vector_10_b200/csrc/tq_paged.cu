@@ -3,10 +3,10 @@
 // the format; the attention kernels are in tq_paged_attend.cu).
 //
 // Both kernels move bytes: 4.25 bits of packed row against 16 (or 32) bits of
-// plain value, a dozen instructions for each value.  A thread owns eight
-// consecutive channels of a row, one 16-byte load (binary16, bfloat16) and
-// one 4-byte word of codes, so a warp reads and writes whole sectors; four
-// lanes share a scale.
+// plain value, some ten instructions for each value.  A thread owns sixteen
+// consecutive channels of a row: one 32-byte load or store of 16-bit values
+// and one 8-byte word of codes, so a warp moves whole sectors, addresses and
+// scales are worked out once for sixteen values, and two lanes share a scale.
 #include <climits>
 #include <cmath>
 #include <cstring>
@@ -39,100 +39,139 @@ __device__ __forceinline__ float scale_value(uint32_t byte) {
 
 // The smallest scale byte with amax <= 7.5 s.  7.5 times a scale has eight
 // bits, so the comparison is exact; the quotient is only a first guess, made
-// a little too small (at most one step for values of up to eleven bits,
-// two for float32).
+// a little too small: at most one step for values of up to eleven bits (the
+// distance of amax / 7.5 from a scale that it is not equal to is then more
+// than the guess is off), two for float32.
+template <int STEPS>
 __device__ __forceinline__ uint32_t scale_byte(float amax) {
     const float y = amax * (0.13333333f * (1.f - 1.f / 1048576.f));
     uint32_t b = y < 6.103515625e-05f ? (uint32_t)(y * 131072.f) : (__float_as_uint(y) >> 20) - 896u;
     b = min(b, PG_MAX_SCALE);
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < STEPS; ++i)
         if (b < PG_MAX_SCALE && 7.5f * scale_value(b) < amax) ++b;
     return b;
 }
 
+// 32 bytes at once, from and to global memory.
+__device__ __forceinline__ void load32(const void *p, uint32_t (&w)[8]) {
+    asm volatile("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                 : "l"(p));
+}
+__device__ __forceinline__ void store32(void *p, const uint32_t (&w)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+                 "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+// The same by halves, where only 16-byte alignment is known.
+__device__ __forceinline__ void load32_16(const void *p, uint32_t (&w)[8]) {
+    const uint4 a = __ldg(static_cast<const uint4 *>(p)), b = __ldg(static_cast<const uint4 *>(p) + 1);
+    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+}
+
+// Plain values of a type: W words hold sixteen of them.
 template <typename T>
-struct Eight;   // eight plain values: load, |max| with a test for finite, store
-
-template <>
-struct Eight<float> {
-    float x[8];
-    __device__ __forceinline__ void load(const float *p) {
-        const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
-        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-    }
-    __device__ __forceinline__ void zero() {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = 0.f;
-    }
-    // bits of the largest magnitude: not finite if >= LIMIT
-    static constexpr uint32_t LIMIT = 0x7F800000u;
-    __device__ __forceinline__ uint32_t amax_bits() const {
-        uint32_t m = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(x[i]) & 0x7FFFFFFFu);
-        return m;
-    }
-    static __device__ __forceinline__ float from_bits(uint32_t b) { return __uint_as_float(b); }
-    __device__ __forceinline__ float get(int i) const { return x[i]; }
-    static __device__ __forceinline__ void store(float *p, const float (&v)[8]) {
-        reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-        reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-    }
+struct Plain {
+    static constexpr int W = sizeof(T) * 4;
+    static constexpr uint32_t LIMIT = sizeof(T) == 4 ? 0x7F800000u : 0;   // |bits| of a value that is not finite
 };
-
-template <typename T>
-struct Eight16 {
-    uint4 w;
-    __device__ __forceinline__ void load(const T *p) { w = __ldg(reinterpret_cast<const uint4 *>(p)); }
-    __device__ __forceinline__ void zero() { w = make_uint4(0, 0, 0, 0); }
-    __device__ __forceinline__ uint32_t amax_bits() const {
-        uint32_t m = __vmaxu2(__vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu),
-                              __vmaxu2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu));
-        return max(m >> 16, m & 0xFFFFu);
-    }
-    __device__ __forceinline__ uint32_t half_word(int i) const {
-        const uint32_t x = i < 2 ? w.x : i < 4 ? w.y : i < 6 ? w.z : w.w;
-        return (i & 1) ? x >> 16 : x & 0xFFFFu;
-    }
-};
-
 template <>
-struct Eight<__half> : Eight16<__half> {
+struct Plain<__half> {
+    static constexpr int W = 8;
     static constexpr uint32_t LIMIT = 0x7C00u;
     static __device__ __forceinline__ float from_bits(uint32_t b) { return __half2float(__ushort_as_half((unsigned short)b)); }
-    __device__ __forceinline__ float get(int i) const { return from_bits(half_word(i)); }
-    static __device__ __forceinline__ void store(__half *p, const float (&v)[8]) {
-        uint32_t o[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
-            o[i] = *reinterpret_cast<const uint32_t *>(&h);
-        }
-        *reinterpret_cast<uint4 *>(p) = make_uint4(o[0], o[1], o[2], o[3]);
-    }
+    static __device__ __forceinline__ float2 pair(uint32_t w) { return __half22float2(tqpaged::u2h(w)); }
 };
-
 template <>
-struct Eight<__nv_bfloat16> : Eight16<__nv_bfloat16> {
+struct Plain<__nv_bfloat16> {
+    static constexpr int W = 8;
     static constexpr uint32_t LIMIT = 0x7F80u;
     static __device__ __forceinline__ float from_bits(uint32_t b) { return __uint_as_float(b << 16); }
-    __device__ __forceinline__ float get(int i) const {
-        const uint32_t x = i < 2 ? w.x : i < 4 ? w.y : i < 6 ? w.z : w.w;
-        return __uint_as_float((i & 1) ? x & 0xFFFF0000u : x << 16);
-    }
-    static __device__ __forceinline__ void store(__nv_bfloat16 *p, const float (&v)[8]) {
-        uint32_t o[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-            o[i] = *reinterpret_cast<const uint32_t *>(&h);
-        }
-        *reinterpret_cast<uint4 *>(p) = make_uint4(o[0], o[1], o[2], o[3]);
+    static __device__ __forceinline__ float2 pair(uint32_t w) {
+        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
     }
 };
 
-// Where a thread's eight channels of row `row` are.
+// |bits| of the largest magnitude; integer order is that of the magnitudes,
+// and infinities and NaN come last.
+template <typename T>
+__device__ __forceinline__ uint32_t amax_bits(const uint32_t (&w)[Plain<T>::W]) {
+    uint32_t m = 0;
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) m = max(m, w[i] & 0x7FFFFFFFu);
+        return m;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = __vmaxu2(m, w[i] & 0x7FFF7FFFu);
+        return max(m >> 16, m & 0xFFFFu);
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ float value(const uint32_t (&w)[Plain<T>::W], int i) {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+    else {
+        const float2 p = Plain<T>::pair(w[i >> 1]);
+        return (i & 1) ? p.y : p.x;
+    }
+}
+
+// The values of eight codes, exact in every type, as words in their order.
+// A nibble is spliced into the mantissa of 1024 + n or 64 + n (binary16), or
+// of 128 + n (bfloat16, whose 136 s has eight bits: 17 times four).
+template <typename T>
+__device__ __forceinline__ void unpack8(uint32_t w, uint32_t byte, uint32_t *o) {
+    using namespace tqpaged;
+    if constexpr (sizeof(T) == 2 && Plain<T>::LIMIT == 0x7F80u) {
+        const __nv_bfloat162 s = __float2bfloat162_rn(scale_value(byte)), m136 = __float2bfloat162_rn(-136.f * scale_value(byte));
+        uint32_t p[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t n = and_or(w >> (4 * i), 0x000F000Fu, 0x43004300u);
+            const __nv_bfloat162 v = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&n), s, m136);
+            p[i] = *reinterpret_cast<const uint32_t *>(&v);
+        }
+        o[0] = __byte_perm(p[0], p[1], 0x5410);
+        o[1] = __byte_perm(p[2], p[3], 0x5410);
+        o[2] = __byte_perm(p[0], p[1], 0x7632);
+        o[3] = __byte_perm(p[2], p[3], 0x7632);
+    } else {
+        // offset and scale in two steps: 72 s can pass the largest binary16
+        const __half2 s = u2h(byte * 0x00800080u), m72 = __float2half2_rn(-72.f), m1032 = __float2half2_rn(-1032.f);
+        const uint32_t w8 = w >> 8;
+        const uint32_t p0 = h2u(__hmul2(__hadd2(u2h(and_or(w, 0x000F000Fu, 0x64006400u)), m1032), s));
+        const uint32_t p1 = h2u(__hmul2(__hadd2(u2h(and_or(w, 0x00F000F0u, 0x54005400u)), m72), s));
+        const uint32_t p2 = h2u(__hmul2(__hadd2(u2h(and_or(w8, 0x000F000Fu, 0x64006400u)), m1032), s));
+        const uint32_t p3 = h2u(__hmul2(__hadd2(u2h(and_or(w8, 0x00F000F0u, 0x54005400u)), m72), s));
+        const uint32_t q[4] = {__byte_perm(p0, p1, 0x5410), __byte_perm(p2, p3, 0x5410), __byte_perm(p0, p1, 0x7632),
+                               __byte_perm(p2, p3, 0x7632)};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (sizeof(T) == 2) {
+                o[i] = q[i];
+            } else {
+                const float2 f = __half22float2(u2h(q[i]));
+                o[2 * i] = __float_as_uint(f.x);
+                o[2 * i + 1] = __float_as_uint(f.y);
+            }
+        }
+    }
+}
+
+// Sixteen values (two words of codes) to plain rows.
+template <typename T>
+__device__ __forceinline__ void store_values(T *dst, uint2 w, uint32_t byte) {
+    uint32_t o[Plain<T>::W];
+    unpack8<T>(w.x, byte, o);
+    unpack8<T>(w.y, byte, o + Plain<T>::W / 2);
+#pragma unroll
+    for (int i = 0; i < Plain<T>::W; i += 8)
+        store32(reinterpret_cast<uint32_t *>(dst) + i, *reinterpret_cast<const uint32_t(*)[8]>(o + i));
+}
+
+// Where a thread's row `base + local` is.
 struct Place {
     int64_t token;
     int head;
@@ -144,25 +183,27 @@ __device__ __forceinline__ Place place_of(const RowsArg &A, int64_t base_token, 
     return {base_token + t, (int)(r - t * (uint32_t)A.H)};
 }
 
-// Quantise one thread's eight values (four lanes share a group, D / 8 a row)
-// and store codes, scale and, if `so`, the stored values.
+// Quantise one thread's sixteen values (two lanes share a group, D / 16 a
+// row) and store codes, scale and, if `so`, the stored values.
 template <typename T, int D>
-__device__ __forceinline__ void quantise_store(Eight<T> x, bool live, bool kept, uint8_t *page, int t, int lg_page, int j,
-                                               T *so, unsigned &bad_rows) {
-    constexpr int LANES = D / 8;
+__device__ __forceinline__ void quantise_store(uint32_t (&x)[Plain<T>::W], bool live, bool kept, uint8_t *page, int t,
+                                               int lg_page, int j, T *so, unsigned &bad_rows) {
+    constexpr int LANES = D / 16;
     const int lane = threadIdx.x & 31;
-    uint32_t m = x.amax_bits();
+    uint32_t m = amax_bits<T>(x);
     // a row with a value that is not finite is stored as zeros
     const uint32_t row_mask = (uint32_t)(((1ull << LANES) - 1) << (lane & ~(LANES - 1)));
-    const bool bad = (__ballot_sync(0xffffffffu, m >= Eight<T>::LIMIT) & row_mask) != 0;
-    if (bad) {
-        x.zero();
+    if (__ballot_sync(0xffffffffu, m >= Plain<T>::LIMIT) & row_mask) {
+#pragma unroll
+        for (int i = 0; i < Plain<T>::W; ++i) x[i] = 0;
         m = 0;
         if (live && j == 0) ++bad_rows;
     }
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    const uint32_t byte = scale_byte(Eight<T>::from_bits(m));
+    float amax;
+    if constexpr (sizeof(T) == 4) amax = __uint_as_float(m);
+    else amax = Plain<T>::from_bits(m);
+    const uint32_t byte = scale_byte<sizeof(T) == 4 ? 2 : 1>(amax);
     const float s = scale_value(byte);
     // Rounding by a first product: x / s of a value with at most 11 bits is
     // either a half-way point n + 1/2 or at least 2^-12 of itself away from
@@ -171,61 +212,67 @@ __device__ __forceinline__ void quantise_store(Eight<T> x, bool live, bool kept,
     // is compared with (n +- 1/2) s, which is exact.
     const float inv = byte ? __fdividef(1.f, s) * (1.f + 1.f / 65536.f) : 0.f;
     constexpr float MAGIC = 12582920.f;   // 1.5 * 2^23 + 8: the sum's low bits are the code + 8
-    float u[8];
+    uint32_t w[2];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float xi = x.get(i);
-        float c = fminf(fmaxf(fmaf(xi, inv, MAGIC), MAGIC - 8.f), MAGIC + 7.f);
-        if (sizeof(T) == 4 && byte) {
-            const float n = fabsf(c - MAGIC), a = fabsf(xi), sg = xi < 0.f ? -1.f : 1.f;
-            if (a < (n - 0.5f) * s) c -= sg;
-            else if (a >= (n + 0.5f) * s) c = fminf(fmaxf(c + sg, MAGIC - 8.f), MAGIC + 7.f);
+    for (int h = 0; h < 2; ++h) {
+        uint32_t acc = 0;
+#pragma unroll
+        for (int i = 7; i >= 0; --i) {
+            const float xi = value<T>(x, 8 * h + i);
+            float c = fminf(fmaxf(fmaf(xi, inv, MAGIC), MAGIC - 8.f), MAGIC + 7.f);
+            if (sizeof(T) == 4 && byte) {
+                const float n = fabsf(c - MAGIC), a = fabsf(xi), sg = xi < 0.f ? -1.f : 1.f;
+                if (a < (n - 0.5f) * s) c -= sg;
+                else if (a >= (n + 0.5f) * s) c = fminf(fmaxf(c + sg, MAGIC - 8.f), MAGIC + 7.f);
+            }
+            acc = acc * 16u + __float_as_uint(c);
         }
-        u[i] = c;
+        // every term but the nibbles: the bits of 1.5 * 2^23, times 16^i
+        w[h] = acc - 0x4B400000u * 0x11111111u;
     }
     if (kept) {
-        uint32_t w = __float_as_uint(u[7]);
-#pragma unroll
-        for (int i = 6; i >= 0; --i) w = w * 16u + __float_as_uint(u[i]);
-        // every term but the nibbles: the bits of 1.5 * 2^23, times 16^i
-        w -= 0x4B400000u * 0x11111111u;
-        *reinterpret_cast<uint32_t *>(page + (int64_t)t * (D / 2) + 4 * j) = w;
-        if ((j & 3) == 0) page[((int64_t)(D / 2) << lg_page) + t * (D / PG_GROUP) + (j >> 2)] = (uint8_t)byte;
+        *reinterpret_cast<uint2 *>(page + (int64_t)t * (D / 2) + 8 * j) = make_uint2(w[0], w[1]);
+        if ((j & 1) == 0) page[((int64_t)(D / 2) << lg_page) + t * (D / PG_GROUP) + (j >> 1)] = (uint8_t)byte;
     }
-    if (so && live) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) u[i] = (u[i] - MAGIC) * s;
-        Eight<T>::store(so, u);
-    }
+    if (so && live) store_values<T>(so, make_uint2(w[0], w[1]), byte);
 }
 
-// Rows -> pages.  Each thread holds eight channels of the key and the value
-// of ROWS rows, all loaded before the first is used.
-template <typename T, int D, int ROWS>
+// Rows -> pages.  Each thread holds sixteen channels of the key and the value
+// of ROWS rows, all loaded before the first is used.  WIDE: every row starts
+// on a 32-byte boundary.
+template <typename T, int D, int ROWS, bool WIDE>
 __global__ void __launch_bounds__(RW_THREADS) tq_paged_write_kernel(const __grid_constant__ RowsArg A) {
-    constexpr int LANES = D / 8, STEP = RW_THREADS / LANES;   // rows a block takes at once
+    constexpr int LANES = D / 16, STEP = RW_THREADS / LANES, W = Plain<T>::W;   // STEP: rows a block takes at once
     const int j = threadIdx.x % LANES, r0 = threadIdx.x / LANES;
     const int64_t base = (int64_t)blockIdx.x * (STEP * ROWS);
     const int64_t base_token = base / A.H;
     const int base_head = (int)(base - base_token * A.H);
     const T *k = static_cast<const T *>(A.k), *v = static_cast<const T *>(A.v);
     T *ko = static_cast<T *>(A.ko), *vo = static_cast<T *>(A.vo);
-    Eight<T> xk[ROWS], xv[ROWS];
+    uint32_t xk[ROWS][W], xv[ROWS][W];
     int64_t slot[ROWS];
     int head[ROWS];
+    auto load = [&](const T *p, uint32_t(&x)[W]) {
+#pragma unroll
+        for (int i = 0; i < W; i += 8) {
+            auto &part = *reinterpret_cast<uint32_t(*)[8]>(x + i);
+            if (WIDE) load32(reinterpret_cast<const uint32_t *>(p) + i, part);
+            else load32_16(reinterpret_cast<const uint32_t *>(p) + i, part);
+        }
+    };
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
         const int local = r0 + i * STEP;
         slot[i] = -1;
         head[i] = 0;
-        xk[i].zero();
-        xv[i].zero();
+#pragma unroll
+        for (int e = 0; e < W; ++e) xk[i][e] = xv[i][e] = 0;
         if (base + local < A.n_rows) {
             const Place p = place_of(A, base_token, base_head, local);
-            slot[i] = A.slots[p.token];
+            slot[i] = __ldg(A.slots + p.token);
             head[i] = p.head;
-            if (k) xk[i].load(k + p.token * A.skt + p.head * A.skh + 8 * j);
-            if (v) xv[i].load(v + p.token * A.svt + p.head * A.svh + 8 * j);
+            if (k) load(k + p.token * A.skt + p.head * A.skh + 16 * j, xk[i]);
+            if (v) load(v + p.token * A.svt + p.head * A.svh + 16 * j, xv[i]);
         }
     }
     unsigned bad_rows = 0;
@@ -237,8 +284,8 @@ __global__ void __launch_bounds__(RW_THREADS) tq_paged_write_kernel(const __grid
         bad_slot |= slot[i] >= A.n_slots;
         const int t = kept ? (int)(slot[i] & ((1 << A.lg_page) - 1)) : 0;
         const int64_t at = kept ? ((slot[i] >> A.lg_page) * A.H + head[i]) * A.page_bytes : 0;
-        if (k) quantise_store<T, D>(xk[i], live, kept, A.kc + at, t, A.lg_page, j, ko ? ko + row * D + 8 * j : nullptr, bad_rows);
-        if (v) quantise_store<T, D>(xv[i], live, kept, A.vc + at, t, A.lg_page, j, vo ? vo + row * D + 8 * j : nullptr, bad_rows);
+        if (k) quantise_store<T, D>(xk[i], live, kept, A.kc + at, t, A.lg_page, j, ko ? ko + row * D + 16 * j : nullptr, bad_rows);
+        if (v) quantise_store<T, D>(xv[i], live, kept, A.vc + at, t, A.lg_page, j, vo ? vo + row * D + 16 * j : nullptr, bad_rows);
     }
     if (bad_rows) atomicAdd(A.status, (unsigned long long)bad_rows);
     if (bad_slot) atomicOr(reinterpret_cast<unsigned int *>(A.status + 1), TQ_FLAG_INDEX);
@@ -248,35 +295,42 @@ __global__ void __launch_bounds__(RW_THREADS) tq_paged_write_kernel(const __grid
 // of zeros.
 template <typename T, int D, int ROWS>
 __global__ void __launch_bounds__(RW_THREADS) tq_paged_read_kernel(const __grid_constant__ RowsArg A) {
-    constexpr int LANES = D / 8, STEP = RW_THREADS / LANES;
+    constexpr int LANES = D / 16, STEP = RW_THREADS / LANES;
     const int j = threadIdx.x % LANES, r0 = threadIdx.x / LANES;
     const int64_t base = (int64_t)blockIdx.x * (STEP * ROWS);
     const int64_t base_token = base / A.H;
     const int base_head = (int)(base - base_token * A.H);
     T *out[2] = {static_cast<T *>(A.ko), static_cast<T *>(A.vo)};
-    uint32_t w[ROWS][2], sb[ROWS][2];
-    bool bad_slot = false;
+    int64_t slot[ROWS];
+    int head[ROWS];
+    uint2 w[ROWS][2];
+    uint32_t sb[ROWS][2];
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
         const int local = r0 + i * STEP;
-        int64_t slot = -1;
-        Place p{0, 0};
+        slot[i] = -1;
+        head[i] = 0;
         if (base + local < A.n_rows) {
-            p = place_of(A, base_token, base_head, local);
-            slot = A.slots[p.token];
+            const Place p = place_of(A, base_token, base_head, local);
+            slot[i] = __ldg(A.slots + p.token);
+            head[i] = p.head;
         }
-        bad_slot |= slot >= A.n_slots;
-        const bool kept = slot >= 0 && slot < A.n_slots;
-        const int t = (int)(slot & ((1 << A.lg_page) - 1));
-        const int64_t at = ((slot >> A.lg_page) * A.H + p.head) * A.page_bytes;
+    }
+    bool bad_slot = false;
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        bad_slot |= slot[i] >= A.n_slots;
+        const bool kept = slot[i] >= 0 && slot[i] < A.n_slots;
+        const int t = (int)(slot[i] & ((1 << A.lg_page) - 1));
+        const int64_t at = ((slot[i] >> A.lg_page) * A.H + head[i]) * A.page_bytes;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const uint8_t *c = h ? A.vc : A.kc;
-            w[i][h] = 0x88888888u;
+            const uint8_t *c = (h ? A.vc : A.kc) + at;
+            w[i][h] = make_uint2(0x88888888u, 0x88888888u);
             sb[i][h] = 0;
             if (kept && out[h]) {
-                w[i][h] = __ldg(reinterpret_cast<const uint32_t *>(c + at + (int64_t)t * (D / 2)) + j);
-                sb[i][h] = __ldg(c + at + ((int64_t)(D / 2) << A.lg_page) + t * (D / PG_GROUP) + (j >> 2));
+                w[i][h] = __ldg(reinterpret_cast<const uint2 *>(c + (int64_t)t * (D / 2)) + j);
+                sb[i][h] = __ldg(c + ((int64_t)(D / 2) << A.lg_page) + t * (D / PG_GROUP) + (j >> 1));
             }
         }
     }
@@ -285,41 +339,40 @@ __global__ void __launch_bounds__(RW_THREADS) tq_paged_read_kernel(const __grid_
         const int64_t row = base + r0 + i * STEP;
         if (row >= A.n_rows) continue;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            if (!out[h]) continue;
-            const float s = scale_value(sb[i][h]);
-            float x[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = (float)((int)((w[i][h] >> (4 * e)) & 15u) - 8) * s;
-            Eight<T>::store(out[h] + row * D + 8 * j, x);
-        }
+        for (int h = 0; h < 2; ++h)
+            if (out[h]) store_values<T>(out[h] + row * D + 16 * j, w[i][h], sb[i][h]);
     }
     if (bad_slot) atomicOr(reinterpret_cast<unsigned int *>(A.status + 1), TQ_FLAG_INDEX);
 }
 
-template <typename T, int D>
+template <typename T, int D, bool WIDE>
 cudaError_t launch_rows(bool write, const RowsArg &A, int n_sms, cudaStream_t stream) {
-    constexpr int STEP = RW_THREADS / (D / 8);
-    // several rows a thread keep more loads in flight; few rows are spread
-    // over as many SMs as they reach
-    constexpr int MANY = sizeof(T) == 4 ? 2 : 4;
+    constexpr int STEP = RW_THREADS / (D / 16);
+    // two rows a thread keep more loads in flight; few rows are spread over
+    // as many SMs as they reach
+    constexpr int MANY = sizeof(T) == 4 ? 1 : 2;
     const bool many = A.n_rows >= (int64_t)STEP * MANY * n_sms * 2;
     const int64_t blocks = (A.n_rows + (many ? STEP * MANY : STEP) - 1) / (many ? STEP * MANY : STEP);
     if (write) {
-        if (many) tq_paged_write_kernel<T, D, MANY><<<(unsigned)blocks, RW_THREADS, 0, stream>>>(A);
-        else tq_paged_write_kernel<T, D, 1><<<(unsigned)blocks, RW_THREADS, 0, stream>>>(A);
+        if (many) tq_paged_write_kernel<T, D, MANY, WIDE><<<(unsigned)blocks, RW_THREADS, 0, stream>>>(A);
+        else tq_paged_write_kernel<T, D, 1, WIDE><<<(unsigned)blocks, RW_THREADS, 0, stream>>>(A);
     } else {
-        if (many) tq_paged_read_kernel<T, D, MANY><<<(unsigned)blocks, RW_THREADS, 0, stream>>>(A);
+        if (many) tq_paged_read_kernel<T, D, 2 * MANY><<<(unsigned)((blocks + 1) / 2), RW_THREADS, 0, stream>>>(A);
         else tq_paged_read_kernel<T, D, 1><<<(unsigned)blocks, RW_THREADS, 0, stream>>>(A);
     }
     return cudaGetLastError();
 }
 
 template <typename T>
-cudaError_t launch_rows_d(int d, bool write, const RowsArg &A, int n_sms, cudaStream_t stream) {
-    if (d == 64) return launch_rows<T, 64>(write, A, n_sms, stream);
-    if (d == 128) return launch_rows<T, 128>(write, A, n_sms, stream);
-    return launch_rows<T, 256>(write, A, n_sms, stream);
+cudaError_t launch_rows_d(int d, bool write, bool wide, const RowsArg &A, int n_sms, cudaStream_t stream) {
+    if (write && !wide) {
+        if (d == 64) return launch_rows<T, 64, false>(write, A, n_sms, stream);
+        if (d == 128) return launch_rows<T, 128, false>(write, A, n_sms, stream);
+        return launch_rows<T, 256, false>(write, A, n_sms, stream);
+    }
+    if (d == 64) return launch_rows<T, 64, true>(write, A, n_sms, stream);
+    if (d == 128) return launch_rows<T, 128, true>(write, A, n_sms, stream);
+    return launch_rows<T, 256, true>(write, A, n_sms, stream);
 }
 
 bool dtype_ok(tq_dtype t) { return t == TQ_F32 || t == TQ_F16 || t == TQ_BF16; }
@@ -368,11 +421,13 @@ tq_status run_rows(tq_paged *ctx, bool write, const tq_pages *pages, RowsArg &A,
     A.n_slots = pages->n_pages * ctx->page;
     A.page_bytes = page_bytes_of(ctx);
     A.status = ctx->d_status;
+    const int64_t es = dtype == TQ_F32 ? 4 : 2;
+    const bool wide = !misaligned(A.k, 32) && !misaligned(A.v, 32) && (A.skt | A.skh | A.svt | A.svh) * es % 32 == 0;
     const int sms = tq_device_sms(ctx->device);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (dtype == TQ_F32) return tq_check_cuda(launch_rows_d<float>(ctx->d, write, A, sms, s));
-    if (dtype == TQ_F16) return tq_check_cuda(launch_rows_d<__half>(ctx->d, write, A, sms, s));
-    return tq_check_cuda(launch_rows_d<__nv_bfloat16>(ctx->d, write, A, sms, s));
+    if (dtype == TQ_F32) return tq_check_cuda(launch_rows_d<float>(ctx->d, write, wide, A, sms, s));
+    if (dtype == TQ_F16) return tq_check_cuda(launch_rows_d<__half>(ctx->d, write, wide, A, sms, s));
+    return tq_check_cuda(launch_rows_d<__nv_bfloat16>(ctx->d, write, wide, A, sms, s));
 }
 
 }  // namespace
@@ -427,7 +482,7 @@ tq_status tq_paged_write(tq_paged *ctx, const void *k, const void *v, tq_dtype d
     if (st != TQ_OK) return st;
     if (!dtype_ok(dtype)) return TQ_ERR_DIM_MISMATCH;
     const int64_t es = dtype == TQ_F32 ? 4 : 2;
-    if (misaligned(k, 16) || misaligned(v, 16) || misaligned(k_stored, 16) || misaligned(v_stored, 16) ||
+    if (misaligned(k, 16) || misaligned(v, 16) || misaligned(k_stored, 32) || misaligned(v_stored, 32) ||
         (k && (stride_kt * es % 16 || stride_kh * es % 16)) || (v && (stride_vt * es % 16 || stride_vh * es % 16)))
         return TQ_ERR_ALIGN;
     RowsArg A = {};
@@ -448,7 +503,7 @@ tq_status tq_paged_read(tq_paged *ctx, const tq_pages *pages, const int64_t *slo
     if (n_tokens != 0 && !k_out && !v_out) return TQ_ERR_NULL;
     tq_status st = check_pages(ctx, pages, k_out != nullptr, v_out != nullptr);
     if (st != TQ_OK) return st;
-    if (misaligned(k_out, 16) || misaligned(v_out, 16)) return TQ_ERR_ALIGN;
+    if (misaligned(k_out, 32) || misaligned(v_out, 32)) return TQ_ERR_ALIGN;
     RowsArg A = {};
     A.ko = k_out;
     A.vo = v_out;
@@ -505,6 +560,7 @@ static tq_status describe(const tq_paged *ctx, const tq_pages *pages, const void
     P.sinks = sinks;
     P.scale_log2 = (scale > 0.f ? scale : 1.f / std::sqrt((float)ctx->d)) * 1.4426950408889634f;
     P.status = ctx->d_status;
+    P.device = ctx->device;
     return TQ_OK;
 }
 

@@ -14,6 +14,8 @@
 // j % 2 of byte j / 2), then [page_size][d/32] scale bytes.
 #pragma once
 
+#include <atomic>
+
 #include "tq_internal.cuh"
 
 #define TQ_FLAG_INDEX 2u   // a slot, page number, length or query start was out of range
@@ -45,6 +47,7 @@ struct PagedAttn {
     void *rec;                       // [grid] tqpaged::Joint
     unsigned long long *status;
     int min_tiles;                   // least tiles a CTA takes
+    int device;
 };
 
 namespace tqpaged {
@@ -373,6 +376,16 @@ __device__ __forceinline__ uint32_t out_pair(const PagedAttn &P, float a, float 
 }
 
 }  // namespace tqpaged
+
+// Allows a kernel `bytes` of dynamic shared memory, once on each device.
+template <typename K>
+cudaError_t tq_paged_allow_smem(K kern, int bytes, int device, std::atomic<uint64_t> &done) {
+    const uint64_t bit = device < 64 ? 1ull << device : 0;
+    if (bit && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
 
 // Kernels of a call: for few rows (queries times heads of a group) of each kv
 // head, and for many; `need` non-null asks for the workspace's bytes only.

@@ -500,7 +500,8 @@ tq_status launch_decode(PagedAttn P, int64_t tiles_bound, int n_sms, cudaStream_
     }
     P.rec = P.part;
     P.part = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(P.part) + rec_bytes);
-    cudaError_t e = cudaFuncSetAttribute(tq_paged_decode_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    static std::atomic<uint64_t> allowed;
+    cudaError_t e = tq_paged_allow_smem(tq_paged_decode_kernel<D, NT>, C::SMEM, P.device, allowed);
     if (e == cudaSuccess) {
         tq_paged_decode_kernel<D, NT><<<grid, THREADS, C::SMEM, stream>>>(P);
         e = cudaGetLastError();

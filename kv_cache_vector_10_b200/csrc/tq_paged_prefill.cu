@@ -436,7 +436,8 @@ tq_status launch_prefill(PagedAttn P, int64_t tiles_bound, int n_sms, cudaStream
     }
     P.rec = P.part;
     P.part = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(P.part) + rec_bytes);
-    cudaError_t e = cudaFuncSetAttribute(tq_paged_prefill_kernel<D, NM>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    static std::atomic<uint64_t> allowed;
+    cudaError_t e = tq_paged_allow_smem(tq_paged_prefill_kernel<D, NM>, C::SMEM, P.device, allowed);
     if (e == cudaSuccess) {
         tq_paged_prefill_kernel<D, NM><<<grid, C::THREADS, C::SMEM, stream>>>(P);
         e = cudaGetLastError();
