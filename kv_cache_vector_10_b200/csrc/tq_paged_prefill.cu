@@ -4,16 +4,15 @@
 //
 // A CTA takes items of 128 NM rows (queries times the query heads of a kv
 // head's group) and walks the tiles of 64 tokens that they see:
-//   S[128 x 64] = Q K^T      Q in TMEM (binary16, pre-scaled rows), K in shared memory
+//   S[128 x 64] = Q K^T      Q (binary16, pre-scaled rows) in TMEM or, where TMEM is full, beside K in shared memory
 //   P = 2^(S - m)            one thread a row: S read from TMEM, P written over it as binary16
 //   O[128 x d] += P V        P from TMEM, V in shared memory (MN-major), O in TMEM
 // What bounds it: 4 * 64 * d operations a row and tile on the tensor cores
 // against 64 exponentials on the special-function units, which take as long
 // at d = 128; and a tile's codes have to be widened to binary16 (about 1.4
 // instructions a code), which is why two row blocks (NM = 2) share each
-// widened tile while TMEM holds both (d <= 128: 2 (d + d/2 + 64) <= 512
-// columns).  With two row blocks one is in its softmax while the other is on
-// the tensor cores; with one, two tiles' scores take turns.
+// widened tile while TMEM holds both (d <= 128).  Two tiles' scores of each
+// row block take turns, so that the next is there when a softmax ends.
 // Roles: NM x 4 softmax warps, 4 widening warps, one warp that requests the
 // codes (bulk copies of pages), one that issues the MMAs.
 #include <algorithm>
@@ -36,19 +35,22 @@ struct Pre {
     using Load = TileLoad<D, PT, 1>;
     static constexpr int KX = PT * 128;              // 64 channels of a tile: rows of 128 bytes, swizzled
     static constexpr int TILE = (D / 64) * KX;
-    static constexpr int OFF_V = NB * TILE, OFF_C = 2 * NB * TILE;
+    // TMEM columns: outputs, two tiles' scores of each row block, and the
+    // queries where they fit (else in shared memory)
+    static constexpr int COL_S = NM * D, COL_Q = COL_S + NM * 2 * PT;
+    static constexpr bool QTMEM = COL_Q + NM * D / 2 <= 512;
+    static constexpr int QX = 128 * 128;             // 64 channels of a row block's queries, swizzled
+    static constexpr int OFF_V = NB * TILE, OFF_Q = 2 * NB * TILE, OFF_C = OFF_Q + (QTMEM ? 0 : NM * (D / 64) * QX);
     static constexpr int SMEM = OFF_C + NC * Load::STAGE + 1024;
-    // TMEM columns
-    static constexpr int COL_Q = NM * D, COL_S = COL_Q + NM * D / 2;
-    static_assert(COL_S + 2 * PT <= 512, "TMEM columns");
+    static_assert(COL_Q <= 512, "TMEM columns");
     static_assert(SMEM <= 232448 - 1024, "shared memory");
 };
 
 struct PreBars {
     uint64_t codes_full[3], codes_free[3];
     uint64_t k_full[3], k_free[3], v_full[3], v_free[3];
-    uint64_t s_full[2], p_full[2];     // a row block's (NM = 2) or a tile parity's (NM = 1) scores, weights
-    uint64_t o_done[2], q_ready[2], done;
+    uint64_t s_full[2][2], p_full[2][2];   // scores and weights of a row block, by the tile's parity
+    uint64_t o_done[2][2], q_ready[2], done;   // o_done by the tile's parity too: two may be outstanding
 };
 
 // D[tmem] (+)= A[tmem] * B[smem desc]^T, kind::f16, one CTA.
@@ -76,6 +78,24 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t saddr, uint32_t lbo) {
 
 __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t phase) {
     return __all_sync(0xffffffffu, tqdev::mbar_wait_bounded(bar, phase));
+}
+
+// Pairs of float32, handled by one instruction.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t r, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
 }
 
 // Bit c of the result: token T0 + c is seen from position p.
@@ -117,9 +137,11 @@ __global__ void __launch_bounds__(Pre<D, NM>::THREADS, 1) tq_paged_prefill_kerne
             tqdev::mbar_init(&bars.v_free[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
-            tqdev::mbar_init(&bars.s_full[i], 1);
-            tqdev::mbar_init(&bars.p_full[i], 4);
-            tqdev::mbar_init(&bars.o_done[i], 1);
+            for (int j = 0; j < 2; ++j) {
+                tqdev::mbar_init(&bars.s_full[i][j], 1);
+                tqdev::mbar_init(&bars.p_full[i][j], 4);
+                tqdev::mbar_init(&bars.o_done[i][j], 1);
+            }
             tqdev::mbar_init(&bars.q_ready[i], 4);
         }
         tqdev::mbar_init(&bars.done, 1);
@@ -175,24 +197,33 @@ __global__ void __launch_bounds__(Pre<D, NM>::THREADS, 1) tq_paged_prefill_kerne
                 for (int i = 0; i < 8; ++i) {
                     uint4 w = active ? __ldg(src + 8 * c + i) : make_uint4(0, 0, 0, 0);
                     if (P.bf16) w = bf16_to_half(w, up);
-                    x[4 * i + 0] = __uint_as_float(__byte_perm(w.x, w.z, 0x5410));
-                    x[4 * i + 1] = __uint_as_float(__byte_perm(w.x, w.z, 0x7632));
-                    x[4 * i + 2] = __uint_as_float(__byte_perm(w.y, w.w, 0x5410));
-                    x[4 * i + 3] = __uint_as_float(__byte_perm(w.y, w.w, 0x7632));
+                    const uint4 o = make_uint4(__byte_perm(w.x, w.z, 0x5410), __byte_perm(w.x, w.z, 0x7632),
+                                               __byte_perm(w.y, w.w, 0x5410), __byte_perm(w.y, w.w, 0x7632));
+                    if (C::QTMEM) {
+                        x[4 * i + 0] = __uint_as_float(o.x);
+                        x[4 * i + 1] = __uint_as_float(o.y);
+                        x[4 * i + 2] = __uint_as_float(o.z);
+                        x[4 * i + 3] = __uint_as_float(o.w);
+                    } else {
+                        const int rr = r & 127;
+                        *reinterpret_cast<uint4 *>(sm + C::OFF_Q + (m * (D / 64) + c) * C::QX + rr * 128 + ((i ^ (rr & 7)) << 4)) = o;
+                    }
                 }
-                tqdev::tmem_st_32x32b_x32(t_q + 32 * c, x);
+                if (C::QTMEM) tqdev::tmem_st_32x32b_x32(t_q + 32 * c, x);
             }
-            tqdev::tmem_wait_st();
-            tqdev::tc_fence_before();
+            if (C::QTMEM) {
+                tqdev::tmem_wait_st();
+                tqdev::tc_fence_before();
+            } else {
+                tqdev::fence_proxy_async_smem();
+            }
             __syncwarp();
             if (lane == 0) tqdev::mbar_arrive(&bars.q_ready[m]);
 
             float m_run = -INFINITY, l_run = 0.f;
             for (int i = it.i0; i < it.i1; ++i, ++n) {
-                const int buf = NM == 2 ? m : n & 1;
-                const uint32_t ph = NM == 2 ? n & 1 : (n >> 1) & 1;
-                const uint32_t t_s = lanes + C::COL_S + buf * PT;
-                if (!wait_warp(&bars.s_full[buf], ph)) {
+                const uint32_t t_s = lanes + C::COL_S + (2 * m + (n & 1)) * PT;
+                if (!wait_warp(&bars.s_full[m][n & 1], (uint32_t)(n >> 1) & 1u)) {
                     failed = true;
                     break;
                 }
@@ -223,7 +254,7 @@ __global__ void __launch_bounds__(Pre<D, NM>::THREADS, 1) tq_paged_prefill_kerne
                     m_run = to;
                     l_run *= f;
                     if (i > it.i0) {   // the output of the tiles before, once it is complete
-                        if (!wait_warp(&bars.o_done[m], (uint32_t)(n - 1) & 1u)) {
+                        if (!wait_warp(&bars.o_done[m][(n - 1) & 1], (uint32_t)((n - 1) >> 1) & 1u)) {
                             failed = true;
                             break;
                         }
@@ -239,25 +270,30 @@ __global__ void __launch_bounds__(Pre<D, NM>::THREADS, 1) tq_paged_prefill_kerne
                     }
                 }
                 const float ref = m_run == -INFINITY ? 0.f : m_run - BIAS;
-                float w[32], l0 = 0.f, l1 = 0.f;
+                float w[32];
+                const uint64_t mul2 = pack2(mul, mul), ref2 = pack2(-ref, -ref);
+                uint64_t l2[2] = {0, 0};
 #pragma unroll
                 for (int c = 0; c < 32; ++c) {
-                    const float a = exp2_fast(fmaf(x[c >> 4][2 * (c & 15)], mul, -ref));
-                    const float b = exp2_fast(fmaf(x[c >> 4][2 * (c & 15) + 1], mul, -ref));
-                    l0 += a;
-                    l1 += b;
+                    float a, b;
+                    unpack2(fma2(pack2(x[c >> 4][2 * (c & 15)], x[c >> 4][2 * (c & 15) + 1]), mul2, ref2), a, b);
+                    a = exp2_fast(a);
+                    b = exp2_fast(b);
+                    l2[c & 1] = add2(l2[c & 1], pack2(a, b));
                     w[c] = __uint_as_float(h2u(__floats2half2_rn(a, b)));
                 }
+                float l0, l1;
+                unpack2(add2(l2[0], l2[1]), l0, l1);
                 l_run += l0 + l1;
                 tqdev::tmem_st_32x32b_x32(t_s, w);
                 tqdev::tmem_wait_st();
                 tqdev::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) tqdev::mbar_arrive(&bars.p_full[buf]);
+                if (lane == 0) tqdev::mbar_arrive(&bars.p_full[m][n & 1]);
             }
             if (failed) break;
             // the item's rows, or this CTA's part of them
-            if (!wait_warp(&bars.o_done[m], (uint32_t)(n - 1) & 1u)) {
+            if (!wait_warp(&bars.o_done[m][(n - 1) & 1], (uint32_t)((n - 1) >> 1) & 1u)) {
                 failed = true;
                 break;
             }
@@ -359,63 +395,97 @@ __global__ void __launch_bounds__(Pre<D, NM>::THREADS, 1) tq_paged_prefill_kerne
         }
         // whatever happened to the others: the copies in flight have landed
         for (int k = max(0, n - NC); k < n; ++k) tqdev::mbar_wait_bounded(&bars.codes_full[k % NC], (uint32_t)(k / NC) & 1u);
-    } else if (lane == 0) {
+    } else {
         // ----------------------------------------------------------------- MMAs
-        const uint32_t id_s = tqdev::idesc_f16_f32(PT), id_o = tqdev::idesc_f16_f32(D) | (1u << 16);   // V is MN-major
-        const uint32_t k0 = tqdev::smem_u32(sm), v0 = k0 + C::OFF_V;
-        auto scores = [&](int kn, int m, int buf) {
-            const uint32_t kb = k0 + (uint32_t)((kn % NB) * C::TILE);
+        // The whole warp walks the loop and one lane issues, so that what the
+        // instructions take as uniform operands is computed as such: with the
+        // loop in one lane the issue of a tile took as long as its products.
+        const bool lead = lane == 0;
+        constexpr uint32_t id_s = tqdev::idesc_f16_f32(PT), id_o = tqdev::idesc_f16_f32(D) | (1u << 16);   // V is MN-major
+        const uint32_t k0 = tqdev::smem_u32(sm);
+        const uint64_t kd0 = tqdev::smem_desc_sw128(k0), qd0 = tqdev::smem_desc_sw128(k0 + C::OFF_Q), vd0 = desc_mn(k0 + C::OFF_V, C::KX);
+        auto scores = [&](int kn, int kb, int m) {
+            const uint32_t t_s = tmem + C::COL_S + (2 * m + (kn & 1)) * PT;
+            const uint64_t kd = kd0 + (uint32_t)(kb * (C::TILE >> 4));
+            if (lead) {
 #pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks)
-                mma_ts(tmem + C::COL_S + buf * PT, tmem + C::COL_Q + m * (D / 2) + 8 * ks,
-                       tqdev::smem_desc_sw128(kb + (ks >> 2) * C::KX + (ks & 3) * 32), id_s, ks != 0);
-            tqdev::mma_commit(&bars.s_full[buf]);
+                for (int ks = 0; ks < D / 16; ++ks) {
+                    const uint64_t b = kd + (uint32_t)(((ks >> 2) * C::KX + (ks & 3) * 32) >> 4);
+                    if (C::QTMEM) mma_ts(t_s, tmem + C::COL_Q + m * (D / 2) + 8 * ks, b, id_s, ks != 0);
+                    else tqdev::mma_f16_ss(t_s, qd0 + (uint32_t)(((m * (D / 64) + (ks >> 2)) * C::QX + (ks & 3) * 32) >> 4), b, id_s, ks != 0);
+                }
+                tqdev::mma_commit(&bars.s_full[m][kn & 1]);
+            }
+            __syncwarp();
         };
-        auto outputs = [&](int vn, int m, int buf, bool first) {
-            const uint32_t vb = v0 + (uint32_t)((vn % NB) * C::TILE);
+        auto outputs = [&](int vn, int vb, int m, bool first) {
+            const uint32_t t_p = tmem + C::COL_S + (2 * m + (vn & 1)) * PT;
+            const uint64_t vd = vd0 + (uint32_t)(vb * (C::TILE >> 4));
+            if (lead) {
+                mma_ts(tmem + m * D, t_p, vd, id_o, !first);
 #pragma unroll
-            for (int ks = 0; ks < PT / 16; ++ks)
-                mma_ts(tmem + m * D, tmem + C::COL_S + buf * PT + 8 * ks, desc_mn(vb + 2048 * ks, C::KX), id_o, !(first && ks == 0));
-            tqdev::mma_commit(&bars.o_done[m]);
+                for (int ks = 1; ks < PT / 16; ++ks) mma_ts(tmem + m * D, t_p + 8 * ks, vd + (uint32_t)((2048 * ks) >> 4), id_o, 1u);
+                tqdev::mma_commit(&bars.o_done[m][vn & 1]);
+            }
+            __syncwarp();
         };
-        auto wait_k = [&](int kn) {
-            const bool ok = tqdev::mbar_wait_bounded(&bars.k_full[kn % NB], (uint32_t)(kn / NB) & 1u);
-            tqdev::tc_fence_after();
-            return ok;
+        auto commit = [&](uint64_t *bar) {
+            if (lead) tqdev::mma_commit(bar);
+            __syncwarp();
         };
-        int n = 0, items = 0;
+        // buffers and phases of the next tile to score (k) and to weigh (v)
+        int n = 0, kn = 0, kb = 0, vb = 0, items = 0;
+        uint32_t kph = 0, vph = 0;
+        auto next_scores = [&]() {
+            if (++kb == NB) {
+                kb = 0;
+                kph ^= 1;
+            }
+            ++kn;
+        };
         bool ok = true;
         for (; it.more() && ok; it.next(P), ++items) {
             const int nt = it.i1 - it.i0;
-            for (int m = 0; m < NM && ok; ++m) ok = tqdev::mbar_wait_bounded(&bars.q_ready[m], (uint32_t)items & 1u);
-            for (int j = 0; j < (NM == 2 ? 1 : 2) && j < nt && ok; ++j) {
-                if (!(ok = wait_k(n + j))) break;
-                for (int m = 0; m < NM; ++m) scores(n + j, m, NM == 2 ? m : (n + j) & 1);
-                tqdev::mma_commit(&bars.k_free[(n + j) % NB]);
+            for (int m = 0; m < NM && ok; ++m) ok = wait_warp(&bars.q_ready[m], (uint32_t)items & 1u);
+            if (!ok) break;
+            tqdev::tc_fence_after();
+            for (int j = 0; j < 2 && j < nt; ++j) {   // two tiles' scores ahead
+                if (!(ok = wait_warp(&bars.k_full[kb], kph))) break;
+                tqdev::tc_fence_after();
+                for (int m = 0; m < NM; ++m) scores(kn, kb, m);
+                commit(&bars.k_free[kb]);
+                next_scores();
             }
             for (int i = 0; i < nt && ok; ++i, ++n) {
+                const bool more = i + 2 < nt;
                 for (int m = 0; m < NM && ok; ++m) {
-                    const int buf = NM == 2 ? m : n & 1;
-                    ok = tqdev::mbar_wait_bounded(&bars.p_full[buf], NM == 2 ? (uint32_t)n & 1u : (uint32_t)(n >> 1) & 1u) &&
-                         (m > 0 || tqdev::mbar_wait_bounded(&bars.v_full[n % NB], (uint32_t)(n / NB) & 1u));
+                    ok = wait_warp(&bars.p_full[m][n & 1], (uint32_t)(n >> 1) & 1u) && (m > 0 || wait_warp(&bars.v_full[vb], vph));
                     if (!ok) break;
                     tqdev::tc_fence_after();
-                    outputs(n, m, buf, i == 0);
-                    const int ahead = NM == 2 ? 1 : 2;
-                    if (i + ahead < nt) {
-                        if (m == 0 && !(ok = wait_k(n + ahead))) break;
-                        scores(n + ahead, m, buf);
+                    outputs(n, vb, m, i == 0);
+                    if (more) {
+                        if (m == 0) {
+                            if (!(ok = wait_warp(&bars.k_full[kb], kph))) break;
+                            tqdev::tc_fence_after();
+                        }
+                        scores(kn, kb, m);
                     }
                 }
                 if (!ok) break;
-                tqdev::mma_commit(&bars.v_free[n % NB]);
-                const int ahead = NM == 2 ? 1 : 2;
-                if (i + ahead < nt) tqdev::mma_commit(&bars.k_free[(n + ahead) % NB]);
+                commit(&bars.v_free[vb]);
+                if (++vb == NB) {
+                    vb = 0;
+                    vph ^= 1;
+                }
+                if (more) {
+                    commit(&bars.k_free[kb]);
+                    next_scores();
+                }
             }
         }
         failed = !ok;
-        tqdev::mma_commit(&bars.done);
-        if (!tqdev::mbar_wait_bounded(&bars.done, 0u)) failed = true;
+        commit(&bars.done);
+        if (!wait_warp(&bars.done, 0u)) failed = true;
     }
     if (failed) atomicOr(reinterpret_cast<unsigned int *>(P.status + 1), TQ_FLAG_WAIT_TIMEOUT);
     tqdev::tc_fence_before();
