@@ -63,6 +63,19 @@ __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_
         : "memory");
 }
 
+// A value that is the same in all lanes, as the compiler can tell.
+template <typename T>
+__device__ __forceinline__ T uniform(T x) {
+    return (T)__shfl_sync(0xffffffffu, (int)x, 0);
+}
+
+// True in one lane of the (whole) warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
 // Descriptor of an MN-major operand in 128-byte swizzled atoms: rows of 64
 // consecutive MN elements, one row per K index, 64-element MN blocks `lbo`
 // bytes apart, 8-row groups 1024 bytes apart.
@@ -125,7 +138,7 @@ __global__ void __launch_bounds__(Pre<D, NM>::THREADS, 1) tq_paged_prefill_kerne
     __shared__ uint32_t s_tmem, s_valid[16];   // s_valid: which parts of a tile were there, 16 tiles back
     __shared__ int s_abort;
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
     tqdev::grid_dep_trigger();
     if (tid == 0) {
         for (int i = 0; i < 3; ++i) {
@@ -157,7 +170,7 @@ __global__ void __launch_bounds__(Pre<D, NM>::THREADS, 1) tq_paged_prefill_kerne
     tqdev::tc_fence_before();
     __syncthreads();
     tqdev::tc_fence_after();
-    const uint32_t tmem = s_tmem;
+    const uint32_t tmem = uniform(s_tmem);
     const int lg_part = min(P.lg_page, 6), parts = PT >> lg_part;
     const uint32_t all_parts = (1u << parts) - 1u;
     bool failed = false;
@@ -397,17 +410,18 @@ __global__ void __launch_bounds__(Pre<D, NM>::THREADS, 1) tq_paged_prefill_kerne
         for (int k = max(0, n - NC); k < n; ++k) tqdev::mbar_wait_bounded(&bars.codes_full[k % NC], (uint32_t)(k / NC) & 1u);
     } else {
         // ----------------------------------------------------------------- MMAs
-        // The whole warp walks the loop and one lane issues, so that what the
-        // instructions take as uniform operands is computed as such: with the
-        // loop in one lane the issue of a tile took as long as its products.
-        const bool lead = lane == 0;
+        // The whole warp walks the loop, on values that the compiler knows to
+        // be the same in all lanes, and an elected lane issues: the operands
+        // of the instructions are then uniform registers.  With the loop in
+        // one lane an issue took 84 cycles, more than the product itself (44
+        // to 65).
         constexpr uint32_t id_s = tqdev::idesc_f16_f32(PT), id_o = tqdev::idesc_f16_f32(D) | (1u << 16);   // V is MN-major
         const uint32_t k0 = tqdev::smem_u32(sm);
         const uint64_t kd0 = tqdev::smem_desc_sw128(k0), qd0 = tqdev::smem_desc_sw128(k0 + C::OFF_Q), vd0 = desc_mn(k0 + C::OFF_V, C::KX);
         auto scores = [&](int kn, int kb, int m) {
             const uint32_t t_s = tmem + C::COL_S + (2 * m + (kn & 1)) * PT;
             const uint64_t kd = kd0 + (uint32_t)(kb * (C::TILE >> 4));
-            if (lead) {
+            if (elect_one()) {
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks) {
                     const uint64_t b = kd + (uint32_t)(((ks >> 2) * C::KX + (ks & 3) * 32) >> 4);
@@ -421,7 +435,7 @@ __global__ void __launch_bounds__(Pre<D, NM>::THREADS, 1) tq_paged_prefill_kerne
         auto outputs = [&](int vn, int vb, int m, bool first) {
             const uint32_t t_p = tmem + C::COL_S + (2 * m + (vn & 1)) * PT;
             const uint64_t vd = vd0 + (uint32_t)(vb * (C::TILE >> 4));
-            if (lead) {
+            if (elect_one()) {
                 mma_ts(tmem + m * D, t_p, vd, id_o, !first);
 #pragma unroll
                 for (int ks = 1; ks < PT / 16; ++ks) mma_ts(tmem + m * D, t_p + 8 * ks, vd + (uint32_t)((2048 * ks) >> 4), id_o, 1u);
@@ -430,7 +444,7 @@ __global__ void __launch_bounds__(Pre<D, NM>::THREADS, 1) tq_paged_prefill_kerne
             __syncwarp();
         };
         auto commit = [&](uint64_t *bar) {
-            if (lead) tqdev::mma_commit(bar);
+            if (elect_one()) tqdev::mma_commit(bar);
             __syncwarp();
         };
         // buffers and phases of the next tile to score (k) and to weigh (v)
@@ -444,8 +458,8 @@ __global__ void __launch_bounds__(Pre<D, NM>::THREADS, 1) tq_paged_prefill_kerne
             ++kn;
         };
         bool ok = true;
-        for (; it.more() && ok; it.next(P), ++items) {
-            const int nt = it.i1 - it.i0;
+        for (; uniform(it.more()) && ok; it.next(P), ++items) {
+            const int nt = uniform(it.i1 - it.i0);
             for (int m = 0; m < NM && ok; ++m) ok = wait_warp(&bars.q_ready[m], (uint32_t)items & 1u);
             if (!ok) break;
             tqdev::tc_fence_after();
