@@ -561,6 +561,7 @@ static tq_status describe(const tq_paged *ctx, const tq_pages *pages, const void
     P.scale_log2 = (scale > 0.f ? scale : 1.f / std::sqrt((float)ctx->d)) * 1.4426950408889634f;
     P.status = ctx->d_status;
     P.device = ctx->device;
+    P.out32 = !misaligned(out, 32) && (stride_ot | stride_oh) % 16 == 0;
     return TQ_OK;
 }
 
@@ -596,7 +597,7 @@ tq_status tq_paged_attention(tq_paged *ctx, const tq_pages *pages, const void *q
     if (total_q == 0) return TQ_OK;
     const size_t need = tq_paged_workspace_bytes(ctx, n_q_heads, pages->n_kv_heads, batch, max_pages, max_q_len);
     if (!workspace || ws_bytes < need) return TQ_ERR_WORKSPACE;
-    if (misaligned(workspace, 16)) return TQ_ERR_ALIGN;
+    if (misaligned(workspace, 32)) return TQ_ERR_ALIGN;
     P.part = static_cast<float *>(workspace);
     return tq_launch_paged_attention(ctx, P, max_q_len, tq_device_sms(ctx->device), static_cast<cudaStream_t>(stream),
                                      nullptr);

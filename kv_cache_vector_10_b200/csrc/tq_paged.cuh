@@ -48,6 +48,7 @@ struct PagedAttn {
     unsigned long long *status;
     int min_tiles;                   // least tiles a CTA takes
     int device;
+    int out32;                       // rows of `out` start on 32-byte boundaries
 };
 
 namespace tqpaged {
@@ -102,14 +103,15 @@ __device__ __forceinline__ int tile_token(const Tiles &t, int i, int TT) {
     return (i < t.ts ? i : t.tw + (i - t.ts)) * TT;
 }
 
-// Tiles of one kv head of a sequence, over its chunks of R rows.
+// Chunks of R rows of one kv head of a sequence, and the tiles of one.
+template <int R>
+__device__ __forceinline__ int chunks_of(const PagedAttn &P, const Seq &s) {
+    return (int)(((long long)s.n * P.G + R - 1) / R);
+}
 template <int R, int TT>
-__device__ __forceinline__ long long head_tiles(const PagedAttn &P, const Seq &s) {
-    long long sum = 0;
-    const long long rows = (long long)s.n * P.G;
-    for (long long r = 0; r < rows; r += R)
-        sum += chunk_tiles<TT>(P, s, (int)r, (int)min(rows, r + R)).n;
-    return sum;
+__device__ __forceinline__ int tiles_of(const PagedAttn &P, const Seq &s, int chunk) {
+    const int row0 = chunk * R;
+    return chunk_tiles<TT>(P, s, row0, min(s.n * P.G, row0 + R)).n;
 }
 
 // This CTA's share of the call's tiles, counted sequence by sequence, kv head
@@ -118,18 +120,44 @@ __device__ __forceinline__ long long head_tiles(const PagedAttn &P, const Seq &s
 // GPU evenly; a chunk cut by a share's border is joined afterwards.
 struct Share {
     long long lo, hi, quota;
-    int b;             // sequence in which lo falls
-    long long into;    // tiles of that sequence before lo
+    int b;              // sequence in which lo falls
+    long long into;     // tiles of that sequence before lo
+    long long per_head; // tiles of one kv head of that sequence
 };
+
+// A thread counts a sequence of few chunks by itself; one of many is counted
+// by its warp.  Call with whole warps.
+template <int R, int TT>
+__device__ __forceinline__ long long head_tiles(const PagedAttn &P, const Seq &s) {
+    constexpr int FEW = 4;
+    const int lane = threadIdx.x & 31, chunks = chunks_of<R>(P, s);
+    long long sum = 0;
+    if (chunks <= FEW)
+        for (int c = 0; c < chunks; ++c) sum += tiles_of<R, TT>(P, s, c);
+    for (uint32_t many = __ballot_sync(0xffffffffu, chunks > FEW); many; many &= many - 1) {
+        const int from = __ffs(many) - 1;
+        const Seq t{0, __shfl_sync(0xffffffffu, s.n, from), __shfl_sync(0xffffffffu, s.len, from)};
+        const int all = chunks_of<R>(P, t);
+        long long part = 0;
+        for (int c = lane; c < all; c += 32) part += tiles_of<R, TT>(P, t, c);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
+        if (lane == from) sum = part;
+    }
+    return sum;
+}
 
 template <int R, int TT, int THREADS>
 __device__ __forceinline__ Share find_share(const PagedAttn &P, Share *s_share, long long *s_sum) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int per = (P.batch + THREADS - 1) / THREADS;
-    const int b0 = min(tid * per, P.batch), b1 = min(b0 + per, P.batch);
+    const int per = (P.batch + THREADS - 1) / THREADS, b0 = tid * per;
     bool bad = false;
-    long long mine = 0;
-    for (int b = b0; b < b1; ++b) mine += head_tiles<R, TT>(P, load_seq(P, b, bad)) * P.Hkv;
+    long long mine = 0, head = 0;
+    for (int i = 0; i < per; ++i) {   // whole warps take the same number of turns
+        const Seq s = b0 + i < P.batch ? load_seq(P, b0 + i, bad) : Seq{0, 0, 0};
+        head = head_tiles<R, TT>(P, s);
+        mine += head * P.Hkv;
+    }
     if (bad) atomicOr(reinterpret_cast<unsigned int *>(P.status + 1), TQ_FLAG_INDEX);
     long long inc = mine;
 #pragma unroll
@@ -146,24 +174,29 @@ __device__ __forceinline__ Share find_share(const PagedAttn &P, Share *s_share, 
         total += s_sum[w];
     }
     const long long first = before + inc - mine;
-    long long quota = (total + gridDim.x - 1) / gridDim.x;
+    long long quota;
+    if (total >> 32) quota = (total + gridDim.x - 1) / gridDim.x;
+    else quota = ((uint32_t)total + gridDim.x - 1) / gridDim.x;
     quota = max(quota, (long long)P.min_tiles);
     const long long lo = min(quota * blockIdx.x, total), hi = min(lo + quota, total);
-    if (tid == 0) *s_share = Share{lo, hi, quota, P.batch, 0};
-    __syncthreads();
-    if (lo < hi && mine > 0 && lo >= first && lo < first + mine) {
-        if (per == 1) *s_share = Share{lo, hi, quota, b0, lo - first};
+    const bool here = lo < hi && lo >= first && lo < first + mine;
+    if (per == 1) {
+        if (here) *s_share = Share{lo, hi, quota, b0, lo - first, head};
+    } else if (__any_sync(0xffffffffu, here)) {
         long long at = first;
-        for (int b = b0; per > 1 && b < b1; ++b) {
-            const long long t = head_tiles<R, TT>(P, load_seq(P, b, bad)) * P.Hkv;
-            if (lo < at + t) {
-                *s_share = Share{lo, hi, quota, b, lo - at};
-                break;
+        bool found = false;
+        for (int i = 0; i < per; ++i) {
+            const Seq s = b0 + i < P.batch ? load_seq(P, b0 + i, bad) : Seq{0, 0, 0};
+            head = head_tiles<R, TT>(P, s);
+            if (here && !found && lo < at + head * P.Hkv) {
+                *s_share = Share{lo, hi, quota, b0 + i, lo - at, head};
+                found = true;
             }
-            at += t;
+            at += head * P.Hkv;
         }
     }
     __syncthreads();
+    if (lo >= hi) return Share{lo, hi, quota, 0, 0, 1};
     return *s_share;
 }
 
@@ -176,6 +209,7 @@ struct Joint {
 
 // The items (chunk of R rows of one kv head of one sequence) that a share
 // reaches, one after another, and the tiles [i0, i1) of each that are its.
+// Whole warps call begin().
 template <int R, int TT>
 struct Walk {
     Seq s;
@@ -190,14 +224,29 @@ struct Walk {
         at = sh.lo;
         hi = sh.hi;
         long long into = sh.into;
-        const long long per_head = head_tiles<R, TT>(P, s);
-        h = (into | per_head) >> 32 ? (int)(into / per_head) : (int)((uint32_t)into / (uint32_t)per_head);
-        into -= h * per_head;
-        for (row0 = 0;; row0 += R) {
-            const int n = chunk_tiles<TT>(P, s, row0, min(s.n * P.G, row0 + R)).n;
-            if (into < n) break;
-            into -= n;
+        h = (into | sh.per_head) >> 32 ? (int)(into / sh.per_head) : (int)((uint32_t)into / (uint32_t)sh.per_head);
+        into -= h * sh.per_head;
+        // the chunk in which the share begins, 32 at a time
+        const int lane = threadIdx.x & 31, chunks = chunks_of<R>(P, s);
+        int c0 = 0;
+        for (;; c0 += 32) {
+            const int mine = c0 + lane < chunks ? tiles_of<R, TT>(P, s, c0 + lane) : 0;
+            long long sum = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long v = __shfl_up_sync(0xffffffffu, sum, o);
+                if (lane >= o) sum += v;
+            }
+            const uint32_t past = __ballot_sync(0xffffffffu, into < sum);
+            if (past || c0 + 32 >= chunks) {
+                const int at_lane = past ? __ffs(past) - 1 : 31;
+                into -= __shfl_sync(0xffffffffu, sum - mine, at_lane);
+                c0 += at_lane;
+                break;
+            }
+            into -= __shfl_sync(0xffffffffu, sum, 31);
         }
+        row0 = c0 * R;
         item(P, (int)into);
     }
     __device__ __forceinline__ bool more() const { return at < hi; }

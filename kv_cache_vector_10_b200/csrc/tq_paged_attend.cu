@@ -524,7 +524,7 @@ tq_status launch_dim(const PagedAttn &P, int max_q_len, int n_sms, cudaStream_t 
 
 tq_status tq_launch_paged_join(int d, const PagedAttn &P, int grid, int rows, cudaStream_t stream) {
     const auto kern = d == 64 ? tq_paged_join_kernel<64> : d == 128 ? tq_paged_join_kernel<128> : tq_paged_join_kernel<256>;
-    return tq_check_cuda(tq_launch_dependent(kern, dim3(grid, std::max(1, rows / 32)), dim3(32 * JOIN_WARPS), 0, stream, P, rows));
+    return tq_check_cuda(tq_launch_dependent(kern, dim3(grid, std::max(1, rows / 8)), dim3(32 * JOIN_WARPS), 0, stream, P, rows));
 }
 
 tq_status tq_launch_paged_attention(const tq_paged *ctx, const PagedAttn &P, int max_q_len, int n_sms,

@@ -24,11 +24,11 @@ namespace {
 using namespace tqpaged;
 
 constexpr int PT = 64;                 // tokens of a tile
-constexpr int WIDEN_WARPS = 4;
 
 template <int D, int NM>
 struct Pre {
-    static constexpr int SOFT_WARPS = 4 * NM, THREADS = 32 * (SOFT_WARPS + WIDEN_WARPS + 2);
+    static constexpr int SOFT_WARPS = 4 * NM, WIDEN_WARPS = NM == 1 ? 8 : 4;   // what 64 K registers allow
+    static constexpr int THREADS = 32 * (SOFT_WARPS + WIDEN_WARPS + 2);
     static constexpr int R = 128 * NM;
     static constexpr int NB = D == 256 ? 2 : 3;      // widened tiles in shared memory
     static constexpr int NC = 3;                     // code tiles in shared memory
@@ -111,6 +111,19 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     return r;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+__device__ __forceinline__ void store32(void *p, uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t e, uint32_t f,
+                                        uint32_t g, uint32_t h) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(a), "r"(b), "r"(c), "r"(d), "r"(e), "r"(f),
+                 "r"(g), "r"(h)
+                 : "memory");
+}
+
 // Bit c of the result: token T0 + c is seen from position p.
 __device__ __forceinline__ uint64_t seen_bits(const PagedAttn &P, int T0, int p, uint32_t got, int lg_part) {
     const int hi = p - T0;
@@ -129,7 +142,7 @@ __device__ __forceinline__ uint64_t seen_bits(const PagedAttn &P, int T0, int p,
 template <int D, int NM>
 __global__ void __launch_bounds__(Pre<D, NM>::THREADS, 1) tq_paged_prefill_kernel(const __grid_constant__ PagedAttn P) {
     using C = Pre<D, NM>;
-    constexpr int NB = C::NB, NC = C::NC, R = C::R, SW = C::SOFT_WARPS;
+    constexpr int NB = C::NB, NC = C::NC, R = C::R, SW = C::SOFT_WARPS, WIDEN_WARPS = C::WIDEN_WARPS;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ __align__(8) PreBars bars;
@@ -195,11 +208,18 @@ __global__ void __launch_bounds__(Pre<D, NM>::THREADS, 1) tq_paged_prefill_kerne
 
             // this row's query: binary16, channels in the order of widen()
             const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(P.q) + (active ? query_at(P, s, it.h, row) : 0));
+            constexpr bool ONCE = D <= 128;   // a row in registers between its maximum and its conversion
+            uint4 qr[ONCE ? D / 8 : 1];
             float up = 1.f, mul = 1.f;
+            if (ONCE) {
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i)
+                    qr[ONCE ? i : 0] = active ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+            }
             if (P.bf16 && active) {
                 uint32_t a = 0;
-#pragma unroll 8
-                for (int i = 0; i < D / 8; ++i) a = __vmaxu2(a, amax4(__ldg(src + i)));
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) a = __vmaxu2(a, amax4(ONCE ? qr[ONCE ? i : 0] : __ldg(src + i)));
                 query_factor(max(a >> 16, a & 0xFFFFu), up, mul);
             }
             mul *= P.scale_log2 * WIDE;
@@ -208,7 +228,7 @@ __global__ void __launch_bounds__(Pre<D, NM>::THREADS, 1) tq_paged_prefill_kerne
                 float x[32];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    uint4 w = active ? __ldg(src + 8 * c + i) : make_uint4(0, 0, 0, 0);
+                    uint4 w = ONCE ? qr[ONCE ? 8 * c + i : 0] : active ? __ldg(src + 8 * c + i) : make_uint4(0, 0, 0, 0);
                     if (P.bf16) w = bf16_to_half(w, up);
                     const uint4 o = make_uint4(__byte_perm(w.x, w.z, 0x5410), __byte_perm(w.x, w.z, 0x7632),
                                                __byte_perm(w.y, w.w, 0x5410), __byte_perm(w.y, w.w, 0x7632));
@@ -256,10 +276,12 @@ __global__ void __launch_bounds__(Pre<D, NM>::THREADS, 1) tq_paged_prefill_kerne
                         if (!((hi >> c) & 1u)) x[1][c] = -INFINITY;
                     }
                 }
-                float mx = -INFINITY;
+                float mc[4];
 #pragma unroll
-                for (int c = 0; c < 32; ++c) mx = fmaxf(mx, fmaxf(x[0][c], x[1][c]));
-                mx *= mul;
+                for (int c = 0; c < 4; ++c) mc[c] = fmaxf(x[0][c], x[1][c]);
+#pragma unroll
+                for (int c = 4; c < 32; ++c) mc[c & 3] = max3(mc[c & 3], x[0][c], x[1][c]);
+                const float mx = fmaxf(max3(mc[0], mc[1], mc[2]), mc[3]) * mul;
                 const bool raise = mx > m_run + RAISE;
                 if (__any_sync(0xffffffffu, raise)) {
                     const float to = fmaxf(m_run, mx);
@@ -320,16 +342,25 @@ __global__ void __launch_bounds__(Pre<D, NM>::THREADS, 1) tq_paged_prefill_kerne
                 float o[32];
                 tqdev::tmem_ld_32x32b_x32(t_o + c, o);
 #pragma unroll
-                for (int e = 0; e < 32; e += 8) {   // columns 0..7 hold channels 0 4 1 5 2 6 3 7
-                    const float4 a = make_float4(o[e] * inv, o[e + 2] * inv, o[e + 4] * inv, o[e + 6] * inv);
-                    const float4 b = make_float4(o[e + 1] * inv, o[e + 3] * inv, o[e + 5] * inv, o[e + 7] * inv);
-                    if (!direct) {
-                        *reinterpret_cast<float4 *>(part + (int64_t)r * D + c + e) = a;
-                        *reinterpret_cast<float4 *>(part + (int64_t)r * D + c + e + 4) = b;
-                    } else if (active) {
-                        *reinterpret_cast<uint4 *>(out + c + e) =
-                            make_uint4(out_pair(P, a.x, a.y), out_pair(P, a.z, a.w), out_pair(P, b.x, b.y), out_pair(P, b.z, b.w));
-                    }
+                for (int e = 0; e < 32; ++e) o[e] *= inv;
+                // columns 0..7 hold channels 0 4 1 5 2 6 3 7
+                if (!direct) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8)
+                        store32(part + (int64_t)r * D + c + e, __float_as_uint(o[e]), __float_as_uint(o[e + 2]), __float_as_uint(o[e + 4]),
+                                __float_as_uint(o[e + 6]), __float_as_uint(o[e + 1]), __float_as_uint(o[e + 3]),
+                                __float_as_uint(o[e + 5]), __float_as_uint(o[e + 7]));
+                } else if (active && P.out32) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 16)
+                        store32(out + c + e, out_pair(P, o[e], o[e + 2]), out_pair(P, o[e + 4], o[e + 6]), out_pair(P, o[e + 1], o[e + 3]),
+                                out_pair(P, o[e + 5], o[e + 7]), out_pair(P, o[e + 8], o[e + 10]), out_pair(P, o[e + 12], o[e + 14]),
+                                out_pair(P, o[e + 9], o[e + 11]), out_pair(P, o[e + 13], o[e + 15]));
+                } else if (active) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8)
+                        *reinterpret_cast<uint4 *>(out + c + e) = make_uint4(out_pair(P, o[e], o[e + 2]), out_pair(P, o[e + 4], o[e + 6]),
+                                                                             out_pair(P, o[e + 1], o[e + 3]), out_pair(P, o[e + 5], o[e + 7]));
                 }
             }
             if (!direct) {
@@ -345,7 +376,8 @@ __global__ void __launch_bounds__(Pre<D, NM>::THREADS, 1) tq_paged_prefill_kerne
         // lanes of a quarter warp take two groups of four tokens, so that
         // their chunks fall into different banks.
         const int e = warp - SW;
-        const int sub = lane & 1, tr = 16 * e + (lane >> 1);   // token row of this lane, every tile
+        const int sub = lane & 1, tr = 16 * (e & 3) + (lane >> 1);   // token row of this lane, every tile
+        constexpr int SPLIT = WIDEN_WARPS / 4;                       // warps that share a row's 64-channel blocks
         const int codes_at = C::Load::codes_at(tr, lg_part), scales_at = C::Load::scales_at(tr, lg_part);
         int n = 0;
         for (; it.more() && !failed; it.next(P)) {
@@ -367,7 +399,9 @@ __global__ void __launch_bounds__(Pre<D, NM>::THREADS, 1) tq_paged_prefill_kerne
                     }
                     uint8_t *dst = sm + (kv ? C::OFF_V : 0) + b * C::TILE + tr * 128;
 #pragma unroll
-                    for (int blk = 0; blk < D / 64; ++blk) {
+                    for (int b0 = 0; b0 < D / 64; b0 += SPLIT) {
+                        const int blk = b0 + e / 4;
+                        if (SPLIT > D / 64 && blk >= D / 64) break;
                         const int grp = 2 * blk + sub;
                         const uint4 w = *reinterpret_cast<const uint4 *>(codes + kv * C::Load::SIDE + codes_at + grp * 16);
                         const uint32_t sb = there ? codes[kv * C::Load::SIDE + scales_at + grp] : 0u;
