@@ -561,6 +561,7 @@ static tq_status describe(const tq_paged *ctx, const tq_pages *pages, const void
     P.scale_log2 = (scale > 0.f ? scale : 1.f / std::sqrt((float)ctx->d)) * 1.4426950408889634f;
     P.status = ctx->d_status;
     P.device = ctx->device;
+    P.inv_G = P.G > 1 ? ~0ull / (uint64_t)P.G + 1 : 0;
     P.out32 = !misaligned(out, 32) && (stride_ot | stride_oh) % 16 == 0;
     return TQ_OK;
 }

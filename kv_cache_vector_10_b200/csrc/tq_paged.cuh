@@ -48,6 +48,7 @@ struct PagedAttn {
     unsigned long long *status;
     int min_tiles;                   // least tiles a CTA takes
     int device;
+    uint64_t inv_G;                  // ceil(2^64 / G), for rows / G (unused at G = 1)
     int out32;                       // rows of `out` start on 32-byte boundaries
 };
 
@@ -73,6 +74,12 @@ __device__ __forceinline__ Seq load_seq(const PagedAttn &P, int b, bool &bad) {
     return s;
 }
 
+// row / G.  The reciprocal is at most G too large in 2^64, so the product's
+// upper half is exact for every 32-bit row.
+__device__ __forceinline__ int token_of(const PagedAttn &P, int row) {
+    return P.G == 1 ? row : (int)__umul64hi((uint64_t)(uint32_t)row, P.inv_G);
+}
+
 // The tiles of TT tokens that the queries of one chunk of rows see: the
 // sinks' tiles [0, ts), then the window's [tw, te).  A chunk that sees
 // nothing has one tile, all of it masked, so that its rows are written.
@@ -85,8 +92,8 @@ template <int TT>
 __device__ __forceinline__ Tiles chunk_tiles(const PagedAttn &P, const Seq &s, int row0, int row1) {
     Tiles t;
     const int base = s.len - s.n;
-    t.p_lo = base + row0 / P.G;
-    t.p_hi = base + (row1 - 1) / P.G;
+    t.p_lo = base + token_of(P, row0);
+    t.p_hi = base + token_of(P, row1 - 1);
     const int hi = max(t.p_hi + 1, 0);
     int lo = 0, s_end = 0;
     if (P.window > 0) {
@@ -229,7 +236,7 @@ struct Walk {
         // the chunk in which the share begins, 32 at a time
         const int lane = threadIdx.x & 31, chunks = chunks_of<R>(P, s);
         int c0 = 0;
-        for (;; c0 += 32) {
+        for (; chunks > 1; c0 += 32) {
             const int mine = c0 + lane < chunks ? tiles_of<R, TT>(P, s, c0 + lane) : 0;
             long long sum = mine;
 #pragma unroll
@@ -408,11 +415,11 @@ __device__ __forceinline__ uint4 bf16_to_half(uint4 w, float up) {
 
 // Element offsets of row `row` of (sequence, kv head) in q and in out.
 __device__ __forceinline__ int64_t query_at(const PagedAttn &P, const Seq &s, int h, int row) {
-    const int tok = row / P.G, hg = row - tok * P.G;
+    const int tok = token_of(P, row), hg = row - tok * P.G;
     return (int64_t)(s.q0 + tok) * P.sqt + (int64_t)(h * P.G + hg) * P.sqh;
 }
 __device__ __forceinline__ int64_t out_at(const PagedAttn &P, const Seq &s, int h, int row) {
-    const int tok = row / P.G, hg = row - tok * P.G;
+    const int tok = token_of(P, row), hg = row - tok * P.G;
     return (int64_t)(s.q0 + tok) * P.sot + (int64_t)(h * P.G + hg) * P.soh;
 }
 

@@ -44,7 +44,7 @@ struct Cfg {
     static constexpr int TT = D == 256 ? 32 : 64;              // tokens of a tile
     static constexpr int NST = D == 64 ? 3 : 2;                // stages: a tile for each warp
     // CTAs of an SM: as many as the registers of the larger fragments allow
-    static constexpr int CTAS = (D == 64 ? 4 : D == 128 ? 3 : 2) - (NT == 2 ? 1 : 0);
+    static constexpr int CTAS = D == 64 ? 4 - NT / 2 : 2;
     using Load = TileLoad<D, TT, NW>;
     static constexpr int SMEM = NST * Load::STAGE;
 };
@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<D, NT>::CTAS) tq_paged_decode_ker
                         const int tok = T0 + 16 * u + tok0 + (e >= 2 ? 8 : 0);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
-                            const int p = s.len - s.n + (it.row0 + 8 * nt + 2 * t + (e & 1)) / P.G;
+                            const int p = s.len - s.n + token_of(P, it.row0 + 8 * nt + 2 * t + (e & 1));
                             const bool see = have && tok <= p && (P.window <= 0 || tok > p - P.window || tok < P.sinks);
                             if (!see) sc[nt][u][e] = -INFINITY;
                         }
@@ -529,7 +529,13 @@ tq_status tq_launch_paged_join(int d, const PagedAttn &P, int grid, int rows, cu
 
 tq_status tq_launch_paged_attention(const tq_paged *ctx, const PagedAttn &P, int max_q_len, int n_sms,
                                     cudaStream_t stream, size_t *need) {
-    if ((int64_t)max_q_len * P.G > 16) return tq_launch_paged_prefill(ctx->d, P, max_q_len, n_sms, stream, need);
+    // Rows of a kv head (the most of a sequence) up to which the fragments of
+    // this file are the faster: at 64 k tokens and 8 kv heads (d = 64) 32 rows
+    // took 43 us here and 59 on the row blocks of 128, 64 rows 68 and 59; at
+    // d = 128 32 rows 62 and 65, 64 rows 109 and 65; at d = 256 (16 k tokens)
+    // 16 rows 37 and 40, 32 rows 53 and 41.
+    const int64_t rows = (int64_t)max_q_len * P.G;
+    if (rows > (ctx->d == 64 ? 48 : 4096 / ctx->d)) return tq_launch_paged_prefill(ctx->d, P, max_q_len, n_sms, stream, need);
     if (ctx->d == 64) return launch_dim<64>(P, max_q_len, n_sms, stream, need);
     if (ctx->d == 128) return launch_dim<128>(P, max_q_len, n_sms, stream, need);
     return launch_dim<256>(P, max_q_len, n_sms, stream, need);

@@ -28,10 +28,15 @@ constexpr int PT = 64;                 // tokens of a tile
 template <int D, int NM>
 struct Pre {
     static constexpr int SOFT_WARPS = 4 * NM, WIDEN_WARPS = NM == 1 ? 8 : 4;   // what 64 K registers allow
-    static constexpr int THREADS = 32 * (SOFT_WARPS + WIDEN_WARPS + 2);
+    // With two row blocks the softmax needs more registers than an equal
+    // share: four warp groups start with 128 a thread and trade them.
+    static constexpr bool TRADE = NM == 2;
+    static constexpr int THREADS = TRADE ? 512 : 32 * (SOFT_WARPS + WIDEN_WARPS + 2);
+    static constexpr int REGS_SOFT = 152, REGS_WIDEN = 104, REGS_REST = 104;
+    static_assert(2 * REGS_SOFT + REGS_WIDEN + REGS_REST <= 512, "registers of the block");
     static constexpr int R = 128 * NM;
     static constexpr int NB = D == 256 ? 2 : 3;      // widened tiles in shared memory
-    static constexpr int NC = 3;                     // code tiles in shared memory
+    static constexpr int NC = 5;                     // code tiles in shared memory (keys run two tiles ahead of values)
     using Load = TileLoad<D, PT, 1>;
     static constexpr int KX = PT * 128;              // 64 channels of a tile: rows of 128 bytes, swizzled
     static constexpr int TILE = (D / 64) * KX;
@@ -47,7 +52,7 @@ struct Pre {
 };
 
 struct PreBars {
-    uint64_t codes_full[3], codes_free[3];
+    uint64_t codes_full[5], codes_free[5];
     uint64_t k_full[3], k_free[3], v_full[3], v_free[3];
     uint64_t s_full[2][2], p_full[2][2];   // scores and weights of a row block, by the tile's parity
     uint64_t o_done[2][2], q_ready[2], done;   // o_done by the tile's parity too: two may be outstanding
@@ -154,12 +159,14 @@ __global__ void __launch_bounds__(Pre<D, NM>::THREADS, 1) tq_paged_prefill_kerne
     const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
     tqdev::grid_dep_trigger();
     if (tid == 0) {
-        for (int i = 0; i < 3; ++i) {
+        for (int i = 0; i < NC; ++i) {
             tqdev::mbar_init(&bars.codes_full[i], 1);
             tqdev::mbar_init(&bars.codes_free[i], WIDEN_WARPS);
-            tqdev::mbar_init(&bars.k_full[i], WIDEN_WARPS);
+        }
+        for (int i = 0; i < 3; ++i) {
+            tqdev::mbar_init(&bars.k_full[i], WIDEN_WARPS / 2);
             tqdev::mbar_init(&bars.k_free[i], 1);
-            tqdev::mbar_init(&bars.v_full[i], WIDEN_WARPS);
+            tqdev::mbar_init(&bars.v_full[i], WIDEN_WARPS / 2);
             tqdev::mbar_init(&bars.v_free[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -192,25 +199,30 @@ __global__ void __launch_bounds__(Pre<D, NM>::THREADS, 1) tq_paged_prefill_kerne
     if (tid == 0) static_cast<Joint *>(P.rec)[blockIdx.x] = it.joint(sh);
 
     if (warp < SW) {
+        if constexpr (C::TRADE) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_SOFT));
         // ------------------------------------------------------------- softmax
         const int m = warp >> 2, r = 128 * m + 32 * (warp & 3) + lane;
         const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
         const uint32_t t_o = lanes + m * D, t_q = lanes + C::COL_Q + m * (D / 2);
-        int n = 0;
-        for (; it.more() && !failed; it.next(P)) {
-            const Seq &s = it.s;
-            const int row = it.row0 + r;
+        // what an item's rows need to know: position of this row's query and
+        // of the row block's first and last, factor of its scores, output
+        int pos = 0, p_lo = 0, p_hi = 0;
+        float mul = 1.f;
+        uint16_t *out = nullptr;   // NULL: no such row
+        auto enter = [&]() {
+            const int row = it.row0 + r, tok = token_of(P, row), hg = row - tok * P.G, base = it.s.len - it.s.n;
             const bool active = row < it.row1;
-            const int pos = s.len - s.n + row / P.G;
-            // positions of the first and last query of this row block
-            const int p_lo = s.len - s.n + (it.row0 + 128 * m) / P.G;
-            const int p_hi = s.len - s.n + (it.row0 + 128 * m + 127) / P.G;
-
+            pos = base + tok;
+            p_lo = base + token_of(P, it.row0 + 128 * m);
+            p_hi = base + token_of(P, it.row0 + 128 * m + 127);
+            const int64_t t64 = it.s.q0 + tok, h64 = it.h * P.G + hg;
+            out = active ? static_cast<uint16_t *>(P.out) + t64 * P.sot + h64 * P.soh : nullptr;
             // this row's query: binary16, channels in the order of widen()
-            const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(P.q) + (active ? query_at(P, s, it.h, row) : 0));
+            const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(P.q) + (active ? t64 * P.sqt + h64 * P.sqh : 0));
             constexpr bool ONCE = D <= 128;   // a row in registers between its maximum and its conversion
             uint4 qr[ONCE ? D / 8 : 1];
-            float up = 1.f, mul = 1.f;
+            float up = 1.f;
+            mul = 1.f;
             if (ONCE) {
 #pragma unroll
                 for (int i = 0; i < D / 8; ++i)
@@ -252,7 +264,10 @@ __global__ void __launch_bounds__(Pre<D, NM>::THREADS, 1) tq_paged_prefill_kerne
             }
             __syncwarp();
             if (lane == 0) tqdev::mbar_arrive(&bars.q_ready[m]);
-
+        };
+        int n = 0;
+        if (it.more()) enter();
+        while (it.more()) {
             float m_run = -INFINITY, l_run = 0.f;
             for (int i = it.i0; i < it.i1; ++i, ++n) {
                 const uint32_t t_s = lanes + C::COL_S + (2 * m + (n & 1)) * PT;
@@ -327,16 +342,19 @@ __global__ void __launch_bounds__(Pre<D, NM>::THREADS, 1) tq_paged_prefill_kerne
                 if (lane == 0) tqdev::mbar_arrive(&bars.p_full[m][n & 1]);
             }
             if (failed) break;
-            // the item's rows, or this CTA's part of them
+            // the next item's queries first, so that its scores are on their
+            // way while this item's rows (or this CTA's part of them) go out
+            const bool direct = it.begins() && it.ends();
+            const float inv = !direct ? WIDE : l_run != 0.f ? WIDE / l_run : 0.f;
+            uint16_t *to = out;
+            float *part = P.part + ((int64_t)blockIdx.x * 2 + (it.begins() ? 1 : 0)) * (R * (D + 2));
+            it.next(P);
+            if (it.more()) enter();
             if (!wait_warp(&bars.o_done[m][(n - 1) & 1], (uint32_t)((n - 1) >> 1) & 1u)) {
                 failed = true;
                 break;
             }
             tqdev::tc_fence_after();
-            const bool direct = it.begins() && it.ends();
-            const float inv = !direct ? WIDE : l_run != 0.f ? WIDE / l_run : 0.f;
-            uint16_t *out = static_cast<uint16_t *>(P.out) + (active ? out_at(P, s, it.h, row) : 0);
-            float *part = P.part + ((int64_t)blockIdx.x * 2 + (it.begins() ? 1 : 0)) * (R * (D + 2));
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
                 float o[32];
@@ -350,16 +368,16 @@ __global__ void __launch_bounds__(Pre<D, NM>::THREADS, 1) tq_paged_prefill_kerne
                         store32(part + (int64_t)r * D + c + e, __float_as_uint(o[e]), __float_as_uint(o[e + 2]), __float_as_uint(o[e + 4]),
                                 __float_as_uint(o[e + 6]), __float_as_uint(o[e + 1]), __float_as_uint(o[e + 3]),
                                 __float_as_uint(o[e + 5]), __float_as_uint(o[e + 7]));
-                } else if (active && P.out32) {
+                } else if (to && P.out32) {
 #pragma unroll
                     for (int e = 0; e < 32; e += 16)
-                        store32(out + c + e, out_pair(P, o[e], o[e + 2]), out_pair(P, o[e + 4], o[e + 6]), out_pair(P, o[e + 1], o[e + 3]),
+                        store32(to + c + e, out_pair(P, o[e], o[e + 2]), out_pair(P, o[e + 4], o[e + 6]), out_pair(P, o[e + 1], o[e + 3]),
                                 out_pair(P, o[e + 5], o[e + 7]), out_pair(P, o[e + 8], o[e + 10]), out_pair(P, o[e + 12], o[e + 14]),
                                 out_pair(P, o[e + 9], o[e + 11]), out_pair(P, o[e + 13], o[e + 15]));
-                } else if (active) {
+                } else if (to) {
 #pragma unroll
                     for (int e = 0; e < 32; e += 8)
-                        *reinterpret_cast<uint4 *>(out + c + e) = make_uint4(out_pair(P, o[e], o[e + 2]), out_pair(P, o[e + 4], o[e + 6]),
+                        *reinterpret_cast<uint4 *>(to + c + e) = make_uint4(out_pair(P, o[e], o[e + 2]), out_pair(P, o[e + 4], o[e + 6]),
                                                                              out_pair(P, o[e + 1], o[e + 3]), out_pair(P, o[e + 5], o[e + 7]));
                 }
             }
@@ -370,42 +388,43 @@ __global__ void __launch_bounds__(Pre<D, NM>::THREADS, 1) tq_paged_prefill_kerne
             tqdev::tc_fence_before();
         }
     } else if (warp < SW + WIDEN_WARPS) {
+        if constexpr (C::TRADE) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_WIDEN));
         // ------------------------------------------------------------ widening
         // A lane takes a group (32 channels) of a token: sixteen bytes of
         // codes to four swizzled sixteen-byte chunks an operand row.  The
         // lanes of a quarter warp take two groups of four tokens, so that
         // their chunks fall into different banks.
-        const int e = warp - SW;
-        const int sub = lane & 1, tr = 16 * (e & 3) + (lane >> 1);   // token row of this lane, every tile
-        constexpr int SPLIT = WIDEN_WARPS / 4;                       // warps that share a row's 64-channel blocks
-        const int codes_at = C::Load::codes_at(tr, lg_part), scales_at = C::Load::scales_at(tr, lg_part);
+        // Half of the warps take the keys, half the values: the keys run two
+        // tiles ahead of the scores and must not wait for the weights, and a
+        // warp makes its writes visible to the MMAs once a tile.
+        constexpr int SIDE_WARPS = WIDEN_WARPS / 2, ROWS = PT / SIDE_WARPS;
+        const int kv = uniform((warp - SW) / SIDE_WARPS), e = (warp - SW) % SIDE_WARPS, sub = lane & 1;
+        uint64_t *full = kv ? bars.v_full : bars.k_full, *freed = kv ? bars.v_free : bars.k_free;
         int n = 0;
         for (; it.more() && !failed; it.next(P)) {
             for (int i = it.i0; i < it.i1; ++i, ++n) {
                 const int cs = n % NC, b = n % NB;
-                if (!wait_warp(&bars.codes_full[cs], (uint32_t)(n / NC) & 1u)) {
+                if (!wait_warp(&bars.codes_full[cs], (uint32_t)(n / NC) & 1u) ||
+                    (n >= NB && !wait_warp(&freed[b], (uint32_t)(n / NB - 1) & 1u))) {
                     failed = true;
                     break;
                 }
-                const uint8_t *codes = sm + C::OFF_C + cs * C::Load::STAGE;
+                const uint8_t *codes = sm + C::OFF_C + cs * C::Load::STAGE + kv * C::Load::SIDE;
+                uint8_t *tile = sm + (kv ? C::OFF_V : 0) + b * C::TILE;
                 const uint32_t got = *reinterpret_cast<volatile uint32_t *>(&s_valid[n & 15]);
-                // a row that holds no token of this sequence may hold anything
-                const bool there = tile_token(it.tl, i, PT) + tr < it.s.len && ((got >> (tr >> lg_part)) & 1u);
+                const int T0 = tile_token(it.tl, i, PT);
 #pragma unroll
-                for (int kv = 0; kv < 2; ++kv) {
-                    if (n >= NB && !wait_warp(kv ? &bars.v_free[b] : &bars.k_free[b], (uint32_t)(n / NB - 1) & 1u)) {
-                        failed = true;
-                        break;
-                    }
-                    uint8_t *dst = sm + (kv ? C::OFF_V : 0) + b * C::TILE + tr * 128;
+                for (int g = 0; g < ROWS; g += 16) {
+                    const int tr = ROWS * e + g + (lane >> 1);   // this lane's token
+                    const uint8_t *src = codes + C::Load::codes_at(tr, lg_part), *scl = codes + C::Load::scales_at(tr, lg_part);
+                    // a row that holds no token of this sequence may hold anything
+                    const bool there = T0 + tr < it.s.len && ((got >> (tr >> lg_part)) & 1u);
+                    uint8_t *dst = tile + tr * 128;
 #pragma unroll
-                    for (int b0 = 0; b0 < D / 64; b0 += SPLIT) {
-                        const int blk = b0 + e / 4;
-                        if (SPLIT > D / 64 && blk >= D / 64) break;
+                    for (int blk = 0; blk < D / 64; ++blk) {
                         const int grp = 2 * blk + sub;
-                        const uint4 w = *reinterpret_cast<const uint4 *>(codes + kv * C::Load::SIDE + codes_at + grp * 16);
-                        const uint32_t sb = there ? codes[kv * C::Load::SIDE + scales_at + grp] : 0u;
-                        const Scale2 sc = scale2(sb * 0x00010001u);
+                        const uint4 w = *reinterpret_cast<const uint4 *>(src + grp * 16);
+                        const Scale2 sc = scale2((there ? scl[grp] : 0u) * 0x00010001u);
                         const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
@@ -415,15 +434,19 @@ __global__ void __launch_bounds__(Pre<D, NM>::THREADS, 1) tq_paged_prefill_kerne
                                 make_uint4(p[0], p[1], p[2], p[3]);
                         }
                     }
-                    tqdev::fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) tqdev::mbar_arrive(kv ? &bars.v_full[b] : &bars.k_full[b]);
                 }
-                if (failed) break;
-                if (lane == 0) tqdev::mbar_arrive(&bars.codes_free[cs]);
+                tqdev::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    tqdev::mbar_arrive(&full[b]);
+                    tqdev::mbar_arrive(&bars.codes_free[cs]);
+                }
             }
         }
-    } else if (warp == SW + WIDEN_WARPS) {
+    } else {
+        if constexpr (C::TRADE) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_REST));
+    }
+    if (warp == SW + WIDEN_WARPS) {
         // ------------------------------------------------- requests of the codes
         const typename C::Load load(P, lane);
         int n = 0;
@@ -442,7 +465,7 @@ __global__ void __launch_bounds__(Pre<D, NM>::THREADS, 1) tq_paged_prefill_kerne
         }
         // whatever happened to the others: the copies in flight have landed
         for (int k = max(0, n - NC); k < n; ++k) tqdev::mbar_wait_bounded(&bars.codes_full[k % NC], (uint32_t)(k / NC) & 1u);
-    } else {
+    } else if (warp == SW + WIDEN_WARPS + 1) {
         // ----------------------------------------------------------------- MMAs
         // The whole warp walks the loop, on values that the compiler knows to
         // be the same in all lanes, and an elected lane issues: the operands
