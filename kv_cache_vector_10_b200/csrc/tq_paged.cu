@@ -243,6 +243,7 @@ __device__ __forceinline__ void quantise_store(uint32_t (&x)[Plain<T>::W], bool 
 template <typename T, int D, int ROWS, bool WIDE>
 __global__ void __launch_bounds__(RW_THREADS) tq_paged_write_kernel(const __grid_constant__ RowsArg A) {
     constexpr int LANES = D / 16, STEP = RW_THREADS / LANES, W = Plain<T>::W;   // STEP: rows a block takes at once
+    tqdev::grid_dep_wait();
     const int j = threadIdx.x % LANES, r0 = threadIdx.x / LANES;
     const int64_t base = (int64_t)blockIdx.x * (STEP * ROWS);
     const int64_t base_token = base / A.H;
@@ -296,6 +297,7 @@ __global__ void __launch_bounds__(RW_THREADS) tq_paged_write_kernel(const __grid
 template <typename T, int D, int ROWS>
 __global__ void __launch_bounds__(RW_THREADS) tq_paged_read_kernel(const __grid_constant__ RowsArg A) {
     constexpr int LANES = D / 16, STEP = RW_THREADS / LANES;
+    tqdev::grid_dep_wait();
     const int j = threadIdx.x % LANES, r0 = threadIdx.x / LANES;
     const int64_t base = (int64_t)blockIdx.x * (STEP * ROWS);
     const int64_t base_token = base / A.H;
@@ -353,14 +355,14 @@ cudaError_t launch_rows(bool write, const RowsArg &A, int n_sms, cudaStream_t st
     constexpr int MANY = sizeof(T) == 4 ? 1 : 2;
     const bool many = A.n_rows >= (int64_t)STEP * MANY * n_sms * 2;
     const int64_t blocks = (A.n_rows + (many ? STEP * MANY : STEP) - 1) / (many ? STEP * MANY : STEP);
-    if (write) {
-        if (many) tq_paged_write_kernel<T, D, MANY, WIDE><<<(unsigned)blocks, RW_THREADS, 0, stream>>>(A);
-        else tq_paged_write_kernel<T, D, 1, WIDE><<<(unsigned)blocks, RW_THREADS, 0, stream>>>(A);
-    } else {
-        if (many) tq_paged_read_kernel<T, D, 2 * MANY><<<(unsigned)((blocks + 1) / 2), RW_THREADS, 0, stream>>>(A);
-        else tq_paged_read_kernel<T, D, 1><<<(unsigned)blocks, RW_THREADS, 0, stream>>>(A);
-    }
-    return cudaGetLastError();
+    // a kernel may be on its way while the one before it ends (it waits for
+    // that one before it reads)
+    const dim3 grid((unsigned)blocks), half((unsigned)((blocks + 1) / 2)), block(RW_THREADS);
+    if (write)
+        return many ? tq_launch_dependent(tq_paged_write_kernel<T, D, MANY, WIDE>, grid, block, 0, stream, A)
+                    : tq_launch_dependent(tq_paged_write_kernel<T, D, 1, WIDE>, grid, block, 0, stream, A);
+    return many ? tq_launch_dependent(tq_paged_read_kernel<T, D, 2 * MANY>, half, block, 0, stream, A)
+                : tq_launch_dependent(tq_paged_read_kernel<T, D, 1>, grid, block, 0, stream, A);
 }
 
 template <typename T>

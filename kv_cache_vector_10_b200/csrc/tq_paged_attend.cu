@@ -148,6 +148,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<D, NT>::CTAS) tq_paged_decode_ker
     static_assert(NW * R * D * 4 <= C::Load::STAGE, "a stage holds the warps' parts of an item");
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    tqdev::grid_dep_wait();
     if (tid == 0) {
         s_abort = tqdev::status_aborted(P.status) ? 1 : 0;
         for (int i = 0; i < NST; ++i) {
@@ -503,8 +504,7 @@ tq_status launch_decode(PagedAttn P, int64_t tiles_bound, int n_sms, cudaStream_
     static std::atomic<uint64_t> allowed;
     cudaError_t e = tq_paged_allow_smem(tq_paged_decode_kernel<D, NT>, C::SMEM, P.device, allowed);
     if (e == cudaSuccess) {
-        tq_paged_decode_kernel<D, NT><<<grid, THREADS, C::SMEM, stream>>>(P);
-        e = cudaGetLastError();
+        e = tq_launch_dependent(tq_paged_decode_kernel<D, NT>, dim3(grid), dim3(THREADS), C::SMEM, stream, P);
     }
     if (e != cudaSuccess || grid == 1) return tq_check_cuda(e);
     return tq_launch_paged_join(D, P, grid, R, stream);

@@ -157,6 +157,7 @@ __global__ void __launch_bounds__(Pre<D, NM>::THREADS, 1) tq_paged_prefill_kerne
     __shared__ int s_abort;
 
     const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
+    tqdev::grid_dep_wait();
     tqdev::grid_dep_trigger();
     if (tid == 0) {
         for (int i = 0; i < NC; ++i) {
@@ -580,8 +581,7 @@ tq_status launch_prefill(PagedAttn P, int64_t tiles_bound, int n_sms, cudaStream
     static std::atomic<uint64_t> allowed;
     cudaError_t e = tq_paged_allow_smem(tq_paged_prefill_kernel<D, NM>, C::SMEM, P.device, allowed);
     if (e == cudaSuccess) {
-        tq_paged_prefill_kernel<D, NM><<<grid, C::THREADS, C::SMEM, stream>>>(P);
-        e = cudaGetLastError();
+        e = tq_launch_dependent(tq_paged_prefill_kernel<D, NM>, dim3(grid), dim3(C::THREADS), C::SMEM, stream, P);
     }
     if (e != cudaSuccess || grid == 1) return tq_check_cuda(e);
     return tq_launch_paged_join(D, P, grid, C::R, stream);
