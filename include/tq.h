@@ -407,7 +407,9 @@ tq_status tq_reset_status(tq_ctx *ctx, void *stream);
  * state but the status word.  Calls that touch the same pages, outputs or
  * workspace at once must be ordered by the caller.  All calls may be captured
  * into graphs, except tq_paged_create, tq_paged_destroy and
- * tq_paged_get_status. */
+ * tq_paged_get_status.  The kernels are programmatic dependent launches: they
+ * may start while the kernel before them in the stream ends, and wait for it
+ * before they read or write. */
 typedef struct tq_paged tq_paged;
 
 /* The pool: two device buffers laid out [n_pages][n_kv_heads] pages of
@@ -440,15 +442,17 @@ int64_t tq_paged_page_bytes(const tq_paged *ctx);
  *             flag bit 1 is set in the status word.  The kept slots of one
  *             call must differ (else the slot holds a mixture of the rows).
  *  k_stored, v_stored : NULL, or device [n_tokens][n_kv_heads][d] in `dtype`,
- *             contiguous, 16-byte aligned: the values that the format keeps
- *             for every row (those with a negative slot too).
+ *             contiguous, 32-byte aligned: the values that the format keeps
+ *             for every row (those with a negative slot too).  They must not
+ *             overlap k or v.
+ * n_tokens below 2^31 and n_tokens * n_kv_heads below 2^33 (TQ_ERR_LIMIT).
  * One kernel. */
 tq_status tq_paged_write(tq_paged *ctx, const void *k, const void *v, tq_dtype dtype, int64_t n_tokens,
                          int64_t stride_kt, int64_t stride_kh, int64_t stride_vt, int64_t stride_vh,
                          const int64_t *slots, const tq_pages *pages, void *k_stored, void *v_stored, void *stream);
 
 /* Read rows back: k_out, v_out device [n_tokens][n_kv_heads][d] in `dtype`,
- * contiguous, 16-byte aligned; either may be NULL.  A slot that is negative
+ * contiguous, 32-byte aligned; either may be NULL.  A slot that is negative
  * or past the pool (flagged) gives rows of zeros.  One kernel. */
 tq_status tq_paged_read(tq_paged *ctx, const tq_pages *pages, const int64_t *slots, int64_t n_tokens, void *k_out,
                         void *v_out, tq_dtype dtype, void *stream);
@@ -476,15 +480,20 @@ tq_status tq_paged_read(tq_paged *ctx, const tq_pages *pages, const int64_t *slo
  *               choice of kernel and the workspace go by it; more queries
  *               than that are still answered.
  *  window     : 0 for none.   scale : 0 for 1/sqrt(d).
- *  workspace  : >= tq_paged_workspace_bytes(...), 16-byte aligned; contents on
- *               entry are ignored.
+ *  workspace  : >= tq_paged_workspace_bytes(...), 32-byte aligned; contents on
+ *               entry are ignored.  Its size depends on the shapes alone.
  * Tokens past a sequence's length may hold anything.  A length outside
  * [0, max_pages * page_size], a query start outside [0, total_q] or a
  * decreasing one is held to those bounds, tokens of a page number outside the
  * pool are not seen, and each sets error flag bit 1 in the status word.
  * n_q_heads <= TQ_MAX_HEADS, batch <= TQ_MAX_PAGED_SEQS, and total_q *
- * n_q_heads and max_pages * page_size below 2^30 (TQ_ERR_LIMIT).  At most two
- * kernels, the second a programmatic dependent launch. */
+ * n_q_heads and max_pages * page_size below 2^30 (TQ_ERR_LIMIT).  Up to two
+ * kernels: few rows of a kv head (its queries times the query heads that share
+ * it: 48 at d = 64, 32 at 128, 16 at 256) are multiplied as register
+ * fragments, more on the tcgen05 tensor cores; the second kernel joins the
+ * sequences that were split.  Results do not depend on the other sequences'
+ * contents, but on how a call's work is split, that is on its shapes and
+ * lengths, in the last bits. */
 size_t tq_paged_workspace_bytes(const tq_paged *ctx, int n_q_heads, int n_kv_heads, int batch, int64_t max_pages,
                                 int max_q_len);
 tq_status tq_paged_attention(tq_paged *ctx, const tq_pages *pages, const void *q, tq_dtype dtype, int64_t total_q,

@@ -527,8 +527,8 @@ static tq_status describe(const tq_paged *ctx, const tq_pages *pages, const void
     if (n_q_heads % pages->n_kv_heads || total_q < 0 || (!q_starts && total_q != batch)) return TQ_ERR_DIM_MISMATCH;
     if (max_pages < 0 || table_stride < max_pages || window < 0 || sinks < 0 || !std::isfinite(scale) || scale < 0.f)
         return TQ_ERR_DIM_MISMATCH;
-    if (n_q_heads > TQ_MAX_HEADS || batch > TQ_MAX_PAGED_SEQS || total_q * n_q_heads > INT_MAX / 2 ||
-        max_pages * ctx->page > INT_MAX / 2 || window > INT_MAX / 2)
+    if (n_q_heads > TQ_MAX_HEADS || batch > TQ_MAX_PAGED_SEQS || total_q > INT_MAX || total_q * n_q_heads > INT_MAX / 2 ||
+        max_pages > INT_MAX || max_pages * ctx->page > INT_MAX / 2 || window > INT_MAX / 2)
         return TQ_ERR_LIMIT;
     if (total_q > 0) {
         if (!q || !out || !seq_lens || (!page_table && max_pages > 0)) return TQ_ERR_NULL;
@@ -573,7 +573,7 @@ extern "C" {
 size_t tq_paged_workspace_bytes(const tq_paged *ctx, int n_q_heads, int n_kv_heads, int batch, int64_t max_pages,
                                 int max_q_len) {
     if (!ctx || n_q_heads <= 0 || n_kv_heads <= 0 || n_q_heads % n_kv_heads || batch <= 0 || max_pages < 0 ||
-        max_q_len <= 0 || max_pages * ctx->page > INT_MAX / 2)
+        max_q_len <= 0 || max_pages > INT_MAX || max_pages * ctx->page > INT_MAX / 2)
         return 0;
     PagedAttn P = {};
     P.Hkv = n_kv_heads;

@@ -497,3 +497,95 @@ def test_prompt_scores_far_apart():
     st = torch.tensor([0, 200], dtype=torch.int32, device=DEV)
     out = cache.attention(q, table, lens_t, q_starts=st, max_q_len=200)
     _check(cache, q, table, lens_t, np.array([0, 200]), out)
+
+
+def test_no_tokens_no_pages_no_queries():
+    cache = tq.PagedCache(2, 1, 64, page_size=16)
+    q = _randn(_gen(1), 3, 2, 64, dtype=torch.float16)
+    zero = torch.zeros(3, dtype=torch.int32, device=DEV)
+    out = cache.attention(q, torch.empty(3, 0, dtype=torch.int32, device=DEV), zero)
+    assert not out.any() and cache.status() == (0, 0)
+    none = cache.attention(q[:0], torch.empty(3, 0, dtype=torch.int32, device=DEV), zero, q_starts=torch.zeros(4, dtype=torch.int32, device=DEV))
+    assert none.shape == (0, 2, 64)
+    with pytest.raises(tq.TQError, match="EMPTY"):
+        cache.attention(q[:0], torch.empty(0, 0, dtype=torch.int32, device=DEV), zero[:0])
+
+
+def test_many_sequences_of_several_queries():
+    """More sequences than a CTA has threads, on both kernels, sequences without queries among them."""
+    B = 700
+    lens = [(11 * i) % 75 for i in range(B)]
+    new = [min(lens[i], i % 4) for i in range(B)]
+    starts = np.concatenate(([0], np.cumsum(new)))
+    cache, table, lens_t, g = _pool(lens, 1, 64, 16, seed=10)
+    q = _randn(g, int(starts[-1]), 2, 64, dtype=torch.float16)
+    st = torch.tensor(starts, dtype=torch.int32, device=DEV)
+    for most in (4, 40):
+        _check(cache, q, table, lens_t, starts, cache.attention(q, table, lens_t, q_starts=st, max_q_len=most))
+
+
+@pytest.mark.parametrize("rows", [1, 40])
+def test_pool_past_four_gigabytes(rows):
+    """Pages whose byte offsets pass 32 bits, written, read and attended to."""
+    H, d, page = 32, 128, 64
+    n_pages = (1 << 32) // (H * page * 68) + 40
+    cache = tq.PagedCache(n_pages, H, d, page_size=page)
+    g = _gen(5)
+    pages = torch.tensor([n_pages - 1, 3, n_pages - 20, n_pages - 7])
+    t = torch.arange(230)
+    slots = (pages[t // page] * page + t % page).to(DEV)
+    k, v = _randn(g, 230, H, d, dtype=torch.float16), _randn(g, 230, H, d, dtype=torch.float16)
+    ks, vs = cache.write(k, v, slots, stored=True)
+    kr, vr = cache.read(slots, dtype=torch.float16)
+    assert torch.equal(kr, ks) and torch.equal(vr, vs)
+    q = _randn(g, rows, H, d, dtype=torch.float16)
+    out = cache.attention(q, pages.int()[None].to(DEV), torch.tensor([230], dtype=torch.int32, device=DEV),
+                          q_starts=torch.tensor([0, rows], dtype=torch.int32, device=DEV), max_q_len=rows)
+    # the same rows in a small pool give the same bits
+    small = tq.PagedCache(4, H, d, page_size=page)
+    small.write(k, v, t.to(DEV))
+    same = small.attention(q, torch.arange(4, dtype=torch.int32, device=DEV)[None], torch.tensor([230], dtype=torch.int32, device=DEV),
+                           q_starts=torch.tensor([0, rows], dtype=torch.int32, device=DEV), max_q_len=rows)
+    assert torch.equal(out, same)
+    assert cache.status() == (0, 0)
+
+
+def test_a_captured_prompt_replays():
+    """Chunks on the tensor cores, captured and replayed with other lengths,
+    pages and queries; a stream of its own."""
+    cache, table, lens_t, g = _pool([500, 300], 1, 128, 32, seed=31)
+    q = _randn(g, 120, 4, 128, dtype=torch.float16)
+    st = torch.tensor([0, 80, 120], dtype=torch.int32, device=DEV)
+    out = torch.empty_like(q)
+    cache.attention(q, table, lens_t, q_starts=st, max_q_len=80, window=200, sinks=3, out=out)
+    torch.cuda.synchronize()
+    graph, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        with torch.cuda.graph(graph, stream=s):
+            cache.attention(q, table, lens_t, q_starts=st, max_q_len=80, window=200, sinks=3, out=out)
+    torch.cuda.current_stream().wait_stream(s)
+    for lens, starts in (([500, 300], [0, 80, 120]), ([77, 300], [0, 5, 120]), ([490, 1], [0, 119, 120])):
+        lens_t.copy_(torch.tensor(lens))
+        st.copy_(torch.tensor(starts))
+        q.copy_(_randn(g, *q.shape, dtype=torch.float16))
+        out.zero_()
+        graph.replay()
+        got = out.clone()
+        torch.cuda.synchronize()
+        _check(cache, q, table, lens_t, np.array(starts), got, window=200, sinks=3)
+        assert torch.equal(got, cache.attention(q, table, lens_t, q_starts=st, max_q_len=80, window=200, sinks=3))
+
+
+def test_workspace_is_checked():
+    cache, table, lens_t, g = _pool([100], 1, 64, 16, seed=2)
+    q = _randn(g, 1, 2, 64, dtype=torch.float16)
+    need = cache.workspace_bytes(2, 1, table.shape[1])
+    ws = torch.empty(need + 32, dtype=torch.uint8, device=DEV)
+    want = cache.attention(q, table, lens_t)
+    ws.fill_(255)                                    # contents on entry are ignored
+    assert torch.equal(cache.attention(q, table, lens_t, workspace=ws[:need]), want)
+    with pytest.raises(tq.TQError, match="WORKSPACE"):
+        cache.attention(q, table, lens_t, workspace=ws[:need - 1])
+    with pytest.raises(tq.TQError, match="ALIGN"):
+        cache.attention(q, table, lens_t, workspace=ws[16:])

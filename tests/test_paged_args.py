@@ -63,7 +63,7 @@ def test_write_refuses():
     assert _write(h, tq.tq_pages(P + 8, P, 10, 2, 0)) == "TQ_ERR_ALIGN"
     assert _write(h, pages, dtype=7) == "TQ_ERR_DIM_MISMATCH"
     assert _write(h, pages, n=-1) == "TQ_ERR_DIM_MISMATCH"
-    for bad in [dict(k=P + 2), dict(v=P + 8), dict(ks=P + 4), dict(sk=(257, 128)), dict(sv=(256, 4))]:
+    for bad in [dict(k=P + 2), dict(v=P + 8), dict(ks=P + 16), dict(sk=(257, 128)), dict(sv=(256, 4))]:
         assert _write(h, pages, **bad) == "TQ_ERR_ALIGN", bad
     assert _write(h, pages, dtype=0, sk=(260, 4)) in PASSED      # float32: multiples of four elements
 
@@ -77,7 +77,8 @@ def test_read_refuses():
     assert read() in PASSED and read(ko=None) in PASSED
     assert read(ko=None, vo=None) == "TQ_ERR_NULL"
     assert read(dtype=3) == "TQ_ERR_DIM_MISMATCH" and read(n=-2) == "TQ_ERR_DIM_MISMATCH"
-    assert read(vo=P + 8) == "TQ_ERR_ALIGN"
+    assert read(vo=P + 16) == "TQ_ERR_ALIGN"
+    assert read(n=1 << 31) in PASSED + ("TQ_ERR_LIMIT",)
     assert read(pages=tq.tq_pages(P, None, 10, 2, 0)) == "TQ_ERR_NULL"
 
 
@@ -101,7 +102,8 @@ def test_attention_refuses():
     for bad in [dict(dtype=0), dict(dtype=5), dict(heads=7), dict(total=-1), dict(starts=None), dict(stride=4), dict(window=-1),
                 dict(sinks=-1), dict(scale=-1.0), dict(scale=float("nan")), dict(pages_max=-1, stride=0)]:
         assert _attend(h, **bad) == "TQ_ERR_DIM_MISMATCH", bad
-    for bad in [dict(heads=2048), dict(batch=70000), dict(total=1 << 28), dict(pages_max=1 << 25, stride=1 << 25)]:
+    for bad in [dict(heads=2048), dict(batch=70000), dict(total=1 << 28), dict(total=1 << 62),
+                dict(pages_max=1 << 25, stride=1 << 25), dict(pages_max=1 << 60, stride=1 << 60), dict(window=1 << 30)]:
         assert _attend(h, **bad) == "TQ_ERR_LIMIT", bad
     for bad in [dict(q=P + 8), dict(out=P + 4), dict(sq=(1028, 128)), dict(so=(1024, 4)), dict(lens=P + 2), dict(starts=P + 1),
                 dict(table=P + 2)]:
@@ -113,7 +115,7 @@ def test_workspace_bytes():
     ws = lambda *a: lib.tq_paged_workspace_bytes(ctypes.byref(h), *a)   # noqa: E731
     assert lib.tq_paged_workspace_bytes(None, 8, 2, 1, 4, 1) == 0
     for bad in [(0, 2, 1, 4, 1), (8, 0, 1, 4, 1), (7, 2, 1, 4, 1), (8, 2, 0, 4, 1), (8, 2, 1, -1, 1), (8, 2, 1, 4, 0),
-                (8, 2, 1, 1 << 25, 1)]:
+                (8, 2, 1, 1 << 25, 1), (8, 2, 1, 1 << 60, 1)]:
         assert ws(*bad) == 0, bad
     assert 0 < ws(8, 2, 1, 4, 1) <= ws(8, 2, 64, 4, 1) <= ws(8, 2, 64, 4000, 1)
     assert ws(1024, 1024, 65535, 1 << 20, 1) < 1 << 26          # bounded by the GPU's size, not by the batch
