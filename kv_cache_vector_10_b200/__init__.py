@@ -472,8 +472,8 @@ class PagedCache:
     quantisation, read back, and attended to through a page table, with an
     optional sliding window and a few first tokens that stay visible.
 
-    k, v: the pool, uint8 [n_pages, n_kv_heads, page bytes].  Token t of page
-    p is slot p * page_size + t.  Calls run on the cache's device, on
+    k, v: the pool, uint8 [n_pages, n_kv_heads, page bytes], to be filled and
+    read in place (not replaced).  Token t of page p is slot p * page_size + t.  Calls run on the cache's device, on
     `stream` or else on that device's current stream; their tensors must be
     on that device.  A call's host work is a few microseconds beside its
     launches, so the checks below are written out rather than shared."""
@@ -500,6 +500,8 @@ class PagedCache:
     def _prepare(self):
         import torch
         self._torch, self._index = torch, self.device.index
+        self._pages = tq_pages(self.k.data_ptr(), self.v.data_ptr(), self.n_pages, self.n_kv_heads, 0)
+        self._pages_ref = ctypes.byref(self._pages)
         self._codes = {torch.float32: TQ_F32, torch.float16: TQ_F16, torch.bfloat16: TQ_BF16}
         self._halves = {torch.float16: TQ_F16, torch.bfloat16: TQ_BF16}
         self._need = {}                                      # workspace bytes by shape
@@ -516,7 +518,7 @@ class PagedCache:
             pass
 
     def struct(self) -> tq_pages:
-        return tq_pages(self.k.data_ptr(), self.v.data_ptr(), self.n_pages, self.n_kv_heads, 0)
+        return self._pages
 
     def _here(self, stream) -> bool:
         """Whether the cache's device is current and `stream` is its current one (None)."""
@@ -551,10 +553,11 @@ class PagedCache:
         ref = v if k is None else k
         if ref is None:
             raise TQError(1, "PagedCache.write")             # TQ_ERR_NULL
-        n, code, dev = len(slots) if slots.dim() else -1, self._codes.get(ref.dtype), self._index
-        shape = (n, self.n_kv_heads, self.head_dim)
+        code, dev = self._codes.get(ref.dtype), self._index
         if code is None or slots.dtype is not torch.int64 or slots.dim() != 1:
             raise TQError(8, "PagedCache.write")             # TQ_ERR_DIM_MISMATCH
+        n = slots.shape[0]
+        shape = (n, self.n_kv_heads, self.head_dim)
         if slots.get_device() != dev:
             raise TQError(12, "PagedCache.write")
         if not slots.is_contiguous():
@@ -581,7 +584,7 @@ class PagedCache:
             if stored:
                 vs = torch.empty_like(v, memory_format=torch.contiguous_format)
                 pvs = vs.data_ptr()
-        err = _lib.tq_paged_write(self.ctx, pk, pv, code, n, skt, skh, svt, svh, slots.data_ptr(), self.struct(),
+        err = _lib.tq_paged_write(self.ctx, pk, pv, code, n, skt, skh, svt, svh, slots.data_ptr(), self._pages_ref,
                                   pks, pvs, torch._C._cuda_getCurrentRawStream(dev))
         if err:
             raise TQError(err, "tq_paged_write")
@@ -601,15 +604,15 @@ class PagedCache:
             raise TQError(12, "PagedCache.read")
         if not slots.is_contiguous():
             slots = slots.contiguous()
-        n = len(slots)
+        n = slots.shape[0]
         kh = vh = pk = pv = None
         if keys:
             kh = slots.new_empty((n, self.n_kv_heads, self.head_dim), dtype=dtype or torch.bfloat16)
             pk = kh.data_ptr()
         if values:
-            vh = slots.new_empty((n, self.n_kv_heads, self.head_dim), dtype=dtype or torch.bfloat16)
+            vh = slots.new_empty((n, self.n_kv_heads, self.head_dim), dtype=dtype or torch.bfloat16) if kh is None else torch.empty_like(kh)
             pv = vh.data_ptr()
-        err = _lib.tq_paged_read(self.ctx, self.struct(), slots.data_ptr(), n, pk, pv, code,
+        err = _lib.tq_paged_read(self.ctx, self._pages_ref, slots.data_ptr(), n, pk, pv, code,
                                  torch._C._cuda_getCurrentRawStream(self._index))
         if err:
             raise TQError(err, "tq_paged_read")
@@ -677,7 +680,7 @@ class PagedCache:
         sqt, sqh, _ = q.stride()
         sot, soh, _ = out.stride()
         err = _lib.tq_paged_attention(
-            self.ctx, self.struct(), q.data_ptr(), code, total, heads, sqt, sqh, page_table.data_ptr(), srow, pages,
+            self.ctx, self._pages_ref, q.data_ptr(), code, total, heads, sqt, sqh, page_table.data_ptr(), srow, pages,
             seq_lens.data_ptr(), starts, batch, most, window, sinks, scale or 0.0, out.data_ptr(), sot, soh,
             workspace.data_ptr(), need, torch._C._cuda_getCurrentRawStream(dev))
         if err:

@@ -391,15 +391,19 @@ __global__ void __launch_bounds__(Pre<D, NM>::THREADS, 1) tq_paged_prefill_kerne
     } else if (warp < SW + WIDEN_WARPS) {
         if constexpr (C::TRADE) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_WIDEN));
         // ------------------------------------------------------------ widening
-        // A lane takes a group (32 channels) of a token: sixteen bytes of
-        // codes to four swizzled sixteen-byte chunks an operand row.  The
-        // lanes of a quarter warp take two groups of four tokens, so that
-        // their chunks fall into different banks.
+        // A lane takes a group (32 channels) of a token: four words of codes
+        // to four swizzled sixteen-byte chunks of an operand row.  The lanes
+        // of a warp take the groups of consecutive tokens in order, and each
+        // begins at another of its words, so that neither the words that are
+        // read at once nor the chunks that eight lanes write fall into the
+        // same banks.  (Shared memory is what the tensor cores, the copies
+        // and this share: at d = 256 a tile takes 1350 cycles of it, and took
+        // 1750 with whole groups read at once.)
         // Half of the warps take the keys, half the values: the keys run two
         // tiles ahead of the scores and must not wait for the weights, and a
         // warp makes its writes visible to the MMAs once a tile.
-        constexpr int SIDE_WARPS = WIDEN_WARPS / 2, ROWS = PT / SIDE_WARPS;
-        const int kv = uniform((warp - SW) / SIDE_WARPS), e = (warp - SW) % SIDE_WARPS, sub = lane & 1;
+        constexpr int SIDE_WARPS = WIDEN_WARPS / 2, ROWS = PT / SIDE_WARPS, GROUPS = D / 32, STEP = 32 / GROUPS;
+        const int kv = uniform((warp - SW) / SIDE_WARPS), e = (warp - SW) % SIDE_WARPS, grp = lane % GROUPS;
         uint64_t *full = kv ? bars.v_full : bars.k_full, *freed = kv ? bars.v_free : bars.k_free;
         int n = 0;
         for (; it.more() && !failed; it.next(P)) {
@@ -415,25 +419,20 @@ __global__ void __launch_bounds__(Pre<D, NM>::THREADS, 1) tq_paged_prefill_kerne
                 const uint32_t got = *reinterpret_cast<volatile uint32_t *>(&s_valid[n & 15]);
                 const int T0 = tile_token(it.tl, i, PT);
 #pragma unroll
-                for (int g = 0; g < ROWS; g += 16) {
-                    const int tr = ROWS * e + g + (lane >> 1);   // this lane's token
-                    const uint8_t *src = codes + C::Load::codes_at(tr, lg_part), *scl = codes + C::Load::scales_at(tr, lg_part);
+                for (int g = 0; g < ROWS; g += STEP) {
+                    const int tr = ROWS * e + g + lane / GROUPS;   // this lane's token
+                    const uint8_t *src = codes + C::Load::codes_at(tr, lg_part) + 16 * grp;
                     // a row that holds no token of this sequence may hold anything
                     const bool there = T0 + tr < it.s.len && ((got >> (tr >> lg_part)) & 1u);
-                    uint8_t *dst = tile + tr * 128;
+                    const Scale2 sc = scale2((there ? codes[C::Load::scales_at(tr, lg_part) + grp] : 0u) * 0x00010001u);
+                    uint8_t *dst = tile + (grp >> 1) * C::KX + tr * 128;
+                    const int first = D == 256 ? (grp >> 1) + tr : D == 128 ? 2 * (grp >> 1) + (tr >> 1) : tr >> 2;
 #pragma unroll
-                    for (int blk = 0; blk < D / 64; ++blk) {
-                        const int grp = 2 * blk + sub;
-                        const uint4 w = *reinterpret_cast<const uint4 *>(src + grp * 16);
-                        const Scale2 sc = scale2((there ? scl[grp] : 0u) * 0x00010001u);
-                        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            uint32_t p[4];
-                            widen(ws[j], sc, p);
-                            *reinterpret_cast<uint4 *>(dst + blk * C::KX + (((4 * sub + j) ^ (tr & 7)) << 4)) =
-                                make_uint4(p[0], p[1], p[2], p[3]);
-                        }
+                    for (int j = 0; j < 4; ++j) {
+                        const int k = (first + j) & 3;
+                        uint32_t p[4];
+                        widen(*reinterpret_cast<const uint32_t *>(src + 4 * k), sc, p);
+                        *reinterpret_cast<uint4 *>(dst + (((4 * (grp & 1) + k) ^ (tr & 7)) << 4)) = make_uint4(p[0], p[1], p[2], p[3]);
                     }
                 }
                 tqdev::fence_proxy_async_smem();
