@@ -47,6 +47,7 @@ struct PagedAttn {
     void *rec;                       // [grid] tqpaged::Joint
     unsigned long long *status;
     int min_tiles;                   // least tiles a CTA takes
+    int item_cost;                   // what beginning an item costs, in tiles
     int device;
     uint64_t inv_G;                  // ceil(2^64 / G), for rows / G (unused at G = 1)
     int out32;                       // rows of `out` start on 32-byte boundaries
@@ -110,7 +111,7 @@ __device__ __forceinline__ int tile_token(const Tiles &t, int i, int TT) {
     return (i < t.ts ? i : t.tw + (i - t.ts)) * TT;
 }
 
-// Chunks of R rows of one kv head of a sequence, and the tiles of one.
+// Chunks of R rows of one kv head of a sequence, and what one costs in tiles.
 template <int R>
 __device__ __forceinline__ int chunks_of(const PagedAttn &P, const Seq &s) {
     return (int)(((long long)s.n * P.G + R - 1) / R);
@@ -118,13 +119,15 @@ __device__ __forceinline__ int chunks_of(const PagedAttn &P, const Seq &s) {
 template <int R, int TT>
 __device__ __forceinline__ int tiles_of(const PagedAttn &P, const Seq &s, int chunk) {
     const int row0 = chunk * R;
-    return chunk_tiles<TT>(P, s, row0, min(s.n * P.G, row0 + R)).n;
+    return chunk_tiles<TT>(P, s, row0, min(s.n * P.G, row0 + R)).n + P.item_cost;
 }
 
-// This CTA's share of the call's tiles, counted sequence by sequence, kv head
-// by kv head, chunk by chunk: [lo, hi) of the whole, and where `lo` falls.
-// Every CTA takes the same number, so a batch of unlike lengths fills the
-// GPU evenly; a chunk cut by a share's border is joined afterwards.
+// This CTA's share of the call's work, counted in tiles sequence by sequence,
+// kv head by kv head, chunk by chunk: [lo, hi) of the whole, and where `lo`
+// falls.  Every CTA takes the same, so a batch of unlike lengths fills the
+// GPU evenly; a chunk cut by a share's border is joined afterwards.  A chunk
+// counts its tiles and, before them, item_cost for its queries and outputs: a
+// border that falls there cuts nothing.
 struct Share {
     long long lo, hi, quota;
     int b;              // sequence in which lo falls
@@ -222,7 +225,9 @@ struct Walk {
     Seq s;
     Tiles tl;
     int b, h, row0, row1, i0, i1;
-    long long at, hi;   // tiles done, end of the share
+    long long at, hi;   // work done, end of the share
+    int span;           // work of this item in the share
+    long long start;    // where the item's work begins
 
     __device__ __forceinline__ void begin(const PagedAttn &P, const Share &sh) {
         bool bad = false;
@@ -260,11 +265,14 @@ struct Walk {
     __device__ __forceinline__ void item(const PagedAttn &P, int into) {
         row1 = min(s.n * P.G, row0 + R);
         tl = chunk_tiles<TT>(P, s, row0, row1);
-        i0 = into;
-        i1 = (int)min((long long)tl.n, into + (hi - at));
+        span = (int)min((long long)(tl.n + P.item_cost - into), hi - at);
+        i0 = max(into - P.item_cost, 0);
+        i1 = max(into + span - P.item_cost, 0);
+        start = at - into;
+        if (i1 == i0) at = hi;   // the border falls before its first tile: the next CTA's
     }
     __device__ __forceinline__ void next(const PagedAttn &P) {
-        at += i1 - i0;
+        at += span;
         if (at >= hi) return;
         row0 += R;
         if (row0 >= s.n * P.G) {
@@ -281,9 +289,9 @@ struct Walk {
     __device__ __forceinline__ bool begins() const { return i0 == 0; }
     __device__ __forceinline__ bool ends() const { return i1 == tl.n; }
     // the note on this share's first item
-    __device__ __forceinline__ Joint joint(const Share &sh) const {
-        const long long start = at - i0;
-        return Joint{row0, begins() ? 0 : row1 - row0, (int)(start / sh.quota), (int)((start + tl.n - 1) / sh.quota), s.q0, h};
+    __device__ __forceinline__ Joint joint(const PagedAttn &P, const Share &sh) const {
+        const long long first = start + P.item_cost;   // where its first tile counts
+        return Joint{row0, !more() || begins() ? 0 : row1 - row0, (int)(first / sh.quota), (int)((first + tl.n - 1) / sh.quota), s.q0, h};
     }
 };
 

@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<D, NT>::CTAS) tq_paged_decode_ker
     it.begin(P, sh);
     if (warp == NW) {
         // --------------------------------------------- requests, items ahead
-        if (lane == 0) static_cast<Joint *>(P.rec)[blockIdx.x] = it.joint(sh);
+        if (lane == 0) static_cast<Joint *>(P.rec)[blockIdx.x] = it.joint(P, sh);
         const typename C::Load load(P, lane);
         int n = 0;
         for (; it.more() && !failed; it.next(P)) {
@@ -493,6 +493,10 @@ tq_status launch_decode(PagedAttn P, int64_t tiles_bound, int n_sms, cudaStream_
     using C = Cfg<D, NT>;
     constexpr int R = 8 * NT;
     P.min_tiles = NW;
+    // loading an item's queries, joining its warps' parts and the groups of
+    // four tiles that it does not fill: drafted tokens 21.1 us without, 18.9
+    // with 4; 4 x 32768 tokens 43.3 and 41.7; 256 items of 64 tiles 43.3 and 44.2
+    P.item_cost = 4;
     const int grid = (int)std::max<int64_t>(1, std::min<int64_t>((int64_t)n_sms * C::CTAS, (tiles_bound + NW - 1) / NW));
     const size_t rec_bytes = ((size_t)grid * sizeof(Joint) + 255) / 256 * 256;
     if (need) {

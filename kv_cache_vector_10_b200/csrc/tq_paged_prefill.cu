@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(Pre<D, NM>::THREADS, 1) tq_paged_prefill_kerne
     bool failed = false;
     Walk<R, PT> it;
     it.begin(P, sh);
-    if (tid == 0) static_cast<Joint *>(P.rec)[blockIdx.x] = it.joint(sh);
+    if (tid == 0) static_cast<Joint *>(P.rec)[blockIdx.x] = it.joint(P, sh);
 
     if (warp < SW) {
         if constexpr (C::TRADE) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_SOFT));
@@ -569,6 +569,10 @@ template <int D, int NM>
 tq_status launch_prefill(PagedAttn P, int64_t tiles_bound, int n_sms, cudaStream_t stream, size_t *need) {
     using C = Pre<D, NM>;
     P.min_tiles = 4;
+    // queries into TMEM and outputs out of it take about as long as eight
+    // tiles: ragged prompts under a window 182 us without, 120 with 4, 112
+    // with 8, 117 with 16; 2048 tokens over 8192 the same within 2%
+    P.item_cost = 8;
     const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(n_sms, (tiles_bound + P.min_tiles - 1) / P.min_tiles));
     const size_t rec_bytes = ((size_t)grid * sizeof(Joint) + 255) / 256 * 256;
     if (need) {
