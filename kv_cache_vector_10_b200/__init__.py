@@ -628,7 +628,7 @@ class PagedCache:
         bfloat16; page_table: int32 [batch, max_pages]; seq_lens: int32
         [batch]; q_starts: int32 [batch + 1], the first query of each sequence
         and the end (None: one query per sequence); max_q_len: the most
-        queries of a sequence (default 1 without q_starts, else total_q);
+        queries of a sequence, as a hint (default their mean);
         window: 0, or how many tokens back a query sees besides the first
         `sinks`; scale: default 1/sqrt(head_dim).  Returns `out` (like q;
         rows of no sequence are not written)."""
@@ -653,7 +653,7 @@ class PagedCache:
                 raise TQError(12, "PagedCache.attention")
             q_starts = q_starts.contiguous()
             starts = q_starts.data_ptr()
-        most = max_q_len or (1 if q_starts is None else max(total, 1))
+        most = max_q_len or (1 if q_starts is None or not batch else max(-(-total // batch), 1))
         q, seq_lens = self._rows(q), seq_lens.contiguous()
         srow, scol = page_table.stride()
         if scol != 1 or srow < pages:

@@ -9,7 +9,15 @@
 // and is used by few rows (queries times query heads of the group), so the
 // floor is the time to read the visible tokens.  At HBM rate an SM has about
 // 94 cycles for 16 tokens, that is some 370 warp instructions to turn 4096
-// codes into operands, multiply and take the softmax.  Hence:
+// codes into operands, multiply and take the softmax; it takes about 290,
+// issued at 0.6 a cycle and scheduler whether 8 or 12 warps are on an SM (the
+// integer pipe, which splices the codes, is the busiest, at 44%).  So a long
+// cache streams at 79% of the copy rate (each further 2^21 tokens of a kv
+// head 55 us, 285 MB), and a call costs about 9 us beside that: its start, the
+// shares, the first tiles' way from memory, the last's way through the warps,
+// and the join.  4 sequences of 32768 tokens, 8 kv heads, 32 query heads, d =
+// 128 (143 MB): 42 us, 51% of the copy rate; one sequence of 1024 tokens and
+// one kv head: 8.2 us.  Hence:
 //   * codes go from shared memory into registers as the fragments of
 //     mma.m16n8k16 (tokens or channels as the 16 rows, queries as the 8
 //     columns) and are widened there: no operand is written back to shared
@@ -19,10 +27,12 @@
 //     channels in the order that this gives; the query's fragments are built
 //     in the same order;
 //   * code pairs are spliced into the mantissa of 1024 + c or 64 + c and
-//     brought to c s by one or two packed operations, exactly;
-//   * each warp streams its own tiles through its own ring of stages, filled
-//     by bulk copies of whole (parts of) pages; warps meet only where an
-//     item ends.
+//     brought to c s by one packed operation, exactly;
+//   * one warp of a CTA requests the codes, a tile for each of the four that
+//     compute, by bulk copies of whole (parts of) pages, and runs ahead of
+//     them across items; those four meet only where an item ends;
+//   * every CTA has the same share of all tiles, whatever the sequences'
+//     lengths; an item cut by a share's border is joined by a second kernel.
 // The probabilities are rounded to binary16 (error 2^-12 of each weight,
 // half a rounding step of a binary16 output); queries are taken to binary16
 // after a power-of-two scaling by their largest channel (bfloat16; exact
@@ -43,7 +53,9 @@ template <int D, int NT>
 struct Cfg {
     static constexpr int TT = D == 256 ? 32 : 64;              // tokens of a tile
     static constexpr int NST = D == 64 ? 3 : 2;                // stages: a tile for each warp
-    // CTAs of an SM: as many as the registers of the larger fragments allow
+    // CTAs of an SM: as many as the registers of the fragments allow (a third
+    // one at d = 128, NT = 1 takes 48 us instead of 43.5 for 4 x 32768 tokens
+    // and 22.1 instead of 20.0 for 4 x 8192)
     static constexpr int CTAS = D == 64 ? 4 - NT / 2 : 2;
     using Load = TileLoad<D, TT, NW>;
     static constexpr int SMEM = NST * Load::STAGE;

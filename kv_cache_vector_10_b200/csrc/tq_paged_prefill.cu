@@ -13,8 +13,15 @@
 // instructions a code), which is why two row blocks (NM = 2) share each
 // widened tile while TMEM holds both (d <= 128).  Two tiles' scores of each
 // row block take turns, so that the next is there when a softmax ends.
-// Roles: NM x 4 softmax warps, 4 widening warps, one warp that requests the
-// codes (bulk copies of pages), one that issues the MMAs.
+// Roles: NM x 4 softmax warps, 4 (NM = 2) or 8 widening warps, one warp that
+// requests the codes (bulk copies of pages), one that issues the MMAs.
+// Measured: 2048 queries over 8192 tokens, 32 query heads on 8 kv heads, d =
+// 128: 270 us, 890 TFLOP/s, 54% of the cuBLAS burst rate.  A tile of both row
+// blocks takes 2150 cycles, of which the tensor cores need 1024 at their best
+// and 1460 for products of 64 columns, shared memory some 1600 (the queries
+// are read from it) and each softmax warp 1800.  Whole prompts of 1674, 3127
+// and 4001 tokens under a window of 1024 with 4 sinks, 8 query heads on 2 kv
+// heads, d = 256: 114 us, 540 TFLOP/s.
 #include <algorithm>
 
 #include "tq_paged.cuh"
