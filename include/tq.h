@@ -481,7 +481,10 @@ tq_status tq_paged_read(tq_paged *ctx, const tq_pages *pages, const int64_t *slo
  *               than that are still answered.
  *  window     : 0 for none.   scale : 0 for 1/sqrt(d).
  *  workspace  : >= tq_paged_workspace_bytes(...), 32-byte aligned; contents on
- *               entry are ignored.  Its size depends on the shapes alone.
+ *               entry are ignored.  Its size depends on the shapes alone; it
+ *               is 0 (and the pointer may be NULL) where max_pages allows only
+ *               short sequences, which are not split, and on invalid
+ *               arguments.
  * Tokens past a sequence's length may hold anything.  A length outside
  * [0, max_pages * page_size], a query start outside [0, total_q] or a
  * decreasing one is held to those bounds, tokens of a page number outside the
@@ -491,7 +494,7 @@ tq_status tq_paged_read(tq_paged *ctx, const tq_pages *pages, const int64_t *slo
  * kernels: few rows of a kv head (its queries times the query heads that share
  * it: 48 at d = 64, 32 at 128, 16 at 256) are multiplied as register
  * fragments, more on the tcgen05 tensor cores; the second kernel joins the
- * sequences that were split.  Results do not depend on the other sequences'
+ * sequences that were split, where there can be such.  Results do not depend on the other sequences'
  * contents, but on how a call's work is split, that is on its shapes and
  * lengths, in the last bits. */
 size_t tq_paged_workspace_bytes(const tq_paged *ctx, int n_q_heads, int n_kv_heads, int batch, int64_t max_pages,

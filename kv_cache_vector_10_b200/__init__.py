@@ -672,7 +672,8 @@ class PagedCache:
                 if len(self._need) > 4096:
                     self._need.clear()
                 need = self._need[key] = self.workspace_bytes(*key)
-            workspace = q.new_empty(need, dtype=torch.uint8)
+            if need:
+                workspace = q.new_empty(need, dtype=torch.uint8)
         elif workspace.get_device() != dev:
             raise TQError(12, "PagedCache.attention")
         else:
@@ -682,7 +683,7 @@ class PagedCache:
         err = _lib.tq_paged_attention(
             self.ctx, self._pages_ref, q.data_ptr(), code, total, heads, sqt, sqh, page_table.data_ptr(), srow, pages,
             seq_lens.data_ptr(), starts, batch, most, window, sinks, scale or 0.0, out.data_ptr(), sot, soh,
-            workspace.data_ptr(), need, torch._C._cuda_getCurrentRawStream(dev))
+            None if workspace is None else workspace.data_ptr(), need, torch._C._cuda_getCurrentRawStream(dev))
         if err:
             raise TQError(err, "tq_paged_attention")
         return out

@@ -568,7 +568,7 @@ tq_status tq_paged_attention(tq_paged *ctx, const tq_pages *pages, const void *q
     if ((st = check_paged_device(ctx)) != TQ_OK) return st;
     if (total_q == 0) return TQ_OK;
     const size_t need = tq_paged_workspace_bytes(ctx, n_q_heads, pages->n_kv_heads, batch, max_pages, max_q_len);
-    if (!workspace || ws_bytes < need) return TQ_ERR_WORKSPACE;
+    if (need && (!workspace || ws_bytes < need)) return TQ_ERR_WORKSPACE;
     if (misaligned(workspace, 32)) return TQ_ERR_ALIGN;
     P.part = static_cast<float *>(workspace);
     return tq_launch_paged_attention(ctx, P, max_q_len, tq_device_sms(ctx->device), static_cast<cudaStream_t>(stream),

@@ -14,6 +14,7 @@
 // j % 2 of byte j / 2), then [page_size][d/32] scale bytes.
 #pragma once
 
+#include <algorithm>
 #include <atomic>
 
 #include "tq_internal.cuh"
@@ -48,6 +49,8 @@ struct PagedAttn {
     unsigned long long *status;
     int min_tiles;                   // least tiles a CTA takes
     int item_cost;                   // what beginning an item costs, in tiles
+    int whole_tokens;                // items of at most so many tokens are not cut (by the kernel)
+    int whole;                       // none is cut: nothing to join, no workspace
     int device;
     uint64_t inv_G;                  // ceil(2^64 / G), for rows / G (unused at G = 1)
     int out32;                       // rows of `out` start on 32-byte boundaries
@@ -127,7 +130,8 @@ __device__ __forceinline__ int tiles_of(const PagedAttn &P, const Seq &s, int ch
 // falls.  Every CTA takes the same, so a batch of unlike lengths fills the
 // GPU evenly; a chunk cut by a share's border is joined afterwards.  A chunk
 // counts its tiles and, before them, item_cost for its queries and outputs: a
-// border that falls there cuts nothing.
+// border that falls there cuts nothing.  Where items stay whole, one belongs to
+// the share in which it begins.
 struct Share {
     long long lo, hi, quota;
     int b;              // sequence in which lo falls
@@ -260,12 +264,14 @@ struct Walk {
         }
         row0 = c0 * R;
         item(P, (int)into);
+        if (P.whole && into > 0) next(P);   // the share before has it
     }
     __device__ __forceinline__ bool more() const { return at < hi; }
     __device__ __forceinline__ void item(const PagedAttn &P, int into) {
         row1 = min(s.n * P.G, row0 + R);
         tl = chunk_tiles<TT>(P, s, row0, row1);
-        span = (int)min((long long)(tl.n + P.item_cost - into), hi - at);
+        const int rest = tl.n + P.item_cost - into;
+        span = P.whole ? rest : (int)min((long long)rest, hi - at);
         i0 = max(into - P.item_cost, 0);
         i1 = max(into + span - P.item_cost, 0);
         start = at - into;
@@ -441,14 +447,39 @@ __device__ __forceinline__ uint32_t out_pair(const PagedAttn &P, float a, float 
 
 }  // namespace tqpaged
 
-// Allows a kernel `bytes` of dynamic shared memory, once on each device.
+// Allows a kernel `bytes` of dynamic shared memory, once on each device; it
+// must have been compiled to `regs` registers a thread or more (a kernel whose
+// warp groups trade registers would wait for what was never there).
 template <typename K>
-cudaError_t tq_paged_allow_smem(K kern, int bytes, int device, std::atomic<uint64_t> &done) {
+cudaError_t tq_paged_allow(K kern, int bytes, int regs, int device, std::atomic<uint64_t> &done) {
     const uint64_t bit = device < 64 ? 1ull << device : 0;
     if (bit && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    cudaFuncAttributes a;
+    cudaError_t e = cudaFuncGetAttributes(&a, kern);
+    if (e == cudaSuccess && a.numRegs < regs) e = cudaErrorLaunchOutOfResources;
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
     return e;
+}
+
+// CTAs of a call of at most `items` items of at most `tiles` tiles, and its
+// workspace: notes for the joining kernel, and two parts of R rows a CTA.
+struct PagedGrid {
+    int ctas;
+    size_t notes, bytes;
+};
+
+inline PagedGrid tq_paged_grid(PagedAttn &P, int64_t items, int64_t tiles, int most_ctas, int R, int D) {
+    P.whole = P.max_tokens <= P.whole_tokens;
+    const int64_t bound = P.whole ? items : (items * tiles + P.min_tiles - 1) / P.min_tiles;
+    PagedGrid g{(int)std::max<int64_t>(1, std::min<int64_t>(most_ctas, bound)), 0, 0};
+    if (g.ctas == 1) P.whole = 1;
+    if (P.whole) return g;
+    g.notes = ((size_t)g.ctas * sizeof(tqpaged::Joint) + 255) / 256 * 256;
+    g.bytes = g.notes + (size_t)g.ctas * 2 * R * (D + 2) * sizeof(float);
+    P.rec = P.part;
+    if (P.part) P.part = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(P.part) + g.notes);
+    return g;
 }
 
 // Kernels of a call: for few rows (queries times heads of a group) of each kv

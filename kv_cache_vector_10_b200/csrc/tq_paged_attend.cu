@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<D, NT>::CTAS) tq_paged_decode_ker
     tqdev::grid_dep_trigger();
     const Share sh = find_share<R, TT, THREADS>(P, &s_share, s_sum);
     if (s_abort || sh.lo >= sh.hi) {
-        if (tid == 0) static_cast<Joint *>(P.rec)[blockIdx.x].rows = 0;
+        if (tid == 0 && !P.whole) static_cast<Joint *>(P.rec)[blockIdx.x].rows = 0;
         return;
     }
     bool failed = false;
@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<D, NT>::CTAS) tq_paged_decode_ker
     it.begin(P, sh);
     if (warp == NW) {
         // --------------------------------------------- requests, items ahead
-        if (lane == 0) static_cast<Joint *>(P.rec)[blockIdx.x] = it.joint(P, sh);
+        if (lane == 0 && !P.whole) static_cast<Joint *>(P.rec)[blockIdx.x] = it.joint(P, sh);
         const typename C::Load load(P, lane);
         int n = 0;
         for (; it.more() && !failed; it.next(P)) {
@@ -501,7 +501,7 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) tq_paged_join_kernel(const __
 }
 
 template <int D, int NT>
-tq_status launch_decode(PagedAttn P, int64_t tiles_bound, int n_sms, cudaStream_t stream, size_t *need) {
+tq_status launch_decode(PagedAttn P, int64_t rows, int n_sms, cudaStream_t stream, size_t *need) {
     using C = Cfg<D, NT>;
     constexpr int R = 8 * NT;
     P.min_tiles = NW;
@@ -509,31 +509,34 @@ tq_status launch_decode(PagedAttn P, int64_t tiles_bound, int n_sms, cudaStream_
     // four tiles that it does not fill: drafted tokens 21.1 us without, 18.9
     // with 4; 4 x 32768 tokens 43.3 and 41.7; 256 items of 64 tiles 43.3 and 44.2
     P.item_cost = 4;
-    const int grid = (int)std::max<int64_t>(1, std::min<int64_t>((int64_t)n_sms * C::CTAS, (tiles_bound + NW - 1) / NW));
-    const size_t rec_bytes = ((size_t)grid * sizeof(Joint) + 255) / 256 * 256;
+    // Uncut, a short item saves the second launch and the join: at d = 128 one
+    // sequence of 512 tokens takes 7.9 us instead of 9.8, of 1024 10.8 instead
+    // of 10.3 (15.1 to 10.9 us with the call's host work), of 2048 16.5 instead
+    // of 10.8; 32 sequences of 1024 tokens 14.9 instead of 19.3.  At d = 64
+    // 1024 tokens 9.8 and 9.5, at d = 256 512 tokens 12.9 and 12.3.
+    P.whole_tokens = 131072 / D;
+    const int64_t items = (int64_t)P.batch * P.Hkv * ((rows + R - 1) / R);
+    const PagedGrid grid = tq_paged_grid(P, items, P.max_tokens / C::TT + 1, n_sms * C::CTAS, R, D);
     if (need) {
-        *need = rec_bytes + (size_t)grid * 2 * R * (D + 2) * sizeof(float);
+        *need = grid.bytes;
         return TQ_OK;
     }
-    P.rec = P.part;
-    P.part = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(P.part) + rec_bytes);
     static std::atomic<uint64_t> allowed;
-    cudaError_t e = tq_paged_allow_smem(tq_paged_decode_kernel<D, NT>, C::SMEM, P.device, allowed);
+    cudaError_t e = tq_paged_allow(tq_paged_decode_kernel<D, NT>, C::SMEM, 0, P.device, allowed);
     if (e == cudaSuccess) {
-        e = tq_launch_dependent(tq_paged_decode_kernel<D, NT>, dim3(grid), dim3(THREADS), C::SMEM, stream, P);
+        e = tq_launch_dependent(tq_paged_decode_kernel<D, NT>, dim3(grid.ctas), dim3(THREADS), C::SMEM, stream, P);
     }
-    if (e != cudaSuccess || grid == 1) return tq_check_cuda(e);
-    return tq_launch_paged_join(D, P, grid, R, stream);
+    if (e != cudaSuccess || P.whole) return tq_check_cuda(e);
+    return tq_launch_paged_join(D, P, grid.ctas, R, stream);
 }
 
 template <int D>
 tq_status launch_dim(const PagedAttn &P, int max_q_len, int n_sms, cudaStream_t stream, size_t *need) {
     const int64_t rows = (int64_t)max_q_len * P.G;
     const int nt = (rows <= 8 || D == 256) ? 1 : 2;
-    const int64_t tiles = (int64_t)P.batch * P.Hkv * ((rows + 8 * nt - 1) / (8 * nt)) * (P.max_tokens / Cfg<D, 1>::TT + 1);
     if constexpr (D != 256)
-        if (nt == 2) return launch_decode<D, 2>(P, tiles, n_sms, stream, need);
-    return launch_decode<D, 1>(P, tiles, n_sms, stream, need);
+        if (nt == 2) return launch_decode<D, 2>(P, rows, n_sms, stream, need);
+    return launch_decode<D, 1>(P, rows, n_sms, stream, need);
 }
 
 }  // namespace

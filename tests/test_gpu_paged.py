@@ -162,8 +162,7 @@ def test_calls_that_are_refused():
     cache.attention(q, table, lens)
     for kw in [dict(q=q.float()), dict(q=q[..., :32]), dict(q=q[:, :3]), dict(q=q[:1]), dict(q=q.cpu()), dict(page_table=table.long()),
                dict(page_table=table[:1]), dict(seq_lens=lens.long()), dict(seq_lens=lens[:1]), dict(q_starts=lens), dict(window=-1),
-               dict(sinks=-1), dict(scale=-1.0), dict(out=torch.empty_like(q).float()), dict(max_q_len=-3),
-               dict(workspace=torch.empty(16, dtype=torch.uint8, device=DEV))]:
+               dict(sinks=-1), dict(scale=-1.0), dict(out=torch.empty_like(q).float()), dict(max_q_len=-3)]:
         with pytest.raises(tq.TQError):
             cache.attention(**(dict(q=q, page_table=table, seq_lens=lens) | kw))
     for args in [(0, 2, 64), (2, 0, 64), (2, 2, 96), (2, 2, 0)]:
@@ -580,7 +579,7 @@ def test_a_captured_prompt_replays():
 
 
 def test_workspace_is_checked():
-    cache, table, lens_t, g = _pool([100], 1, 64, 16, seed=2)
+    cache, table, lens_t, g = _pool([4000], 1, 64, 16, seed=2)
     q = _randn(g, 1, 2, 64, dtype=torch.float16)
     need = cache.workspace_bytes(2, 1, table.shape[1])
     ws = torch.empty(need + 32, dtype=torch.uint8, device=DEV)
@@ -591,3 +590,23 @@ def test_workspace_is_checked():
         cache.attention(q, table, lens_t, workspace=ws[:need - 1])
     with pytest.raises(tq.TQError, match="ALIGN"):
         cache.attention(q, table, lens_t, workspace=ws[16:])
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("most", [1, 50])
+def test_short_sequences_whole_or_split(d, most):
+    """Where the page table allows only short sequences none is split and no
+    workspace is needed; a wider table, the same sequences: split and joined."""
+    lens, new = [500, 3, 256, 0, 77, 130], [min(n, most) for n in (50, 3, 17, 1, 1, 40)]
+    starts = np.concatenate(([0], np.cumsum(new)))
+    cache, table, lens_t, g = _pool(lens, 2, d, 16, seed=d + most, dtype=torch.bfloat16)
+    table = table[:, :32].contiguous()
+    wide = torch.cat((table, torch.full((len(lens), 4096 // 16), -1, dtype=torch.int32, device=DEV)), 1)
+    assert cache.workspace_bytes(8, len(lens), 32, most) == 0 < cache.workspace_bytes(8, len(lens), wide.shape[1], most)
+    q = _randn(g, int(starts[-1]), 8, d, dtype=torch.bfloat16)
+    st = torch.tensor(starts, dtype=torch.int32, device=DEV)
+    for t in (table, wide):
+        for window, sinks in ((0, 0), (100, 2)):
+            out = cache.attention(q, t, lens_t, q_starts=st, max_q_len=most, window=window, sinks=sinks)
+            _check(cache, q, table, lens_t, starts, out, window=window, sinks=sinks)
+    assert cache.status() == (0, 0)

@@ -117,7 +117,9 @@ def test_workspace_bytes():
     for bad in [(0, 2, 1, 4, 1), (8, 0, 1, 4, 1), (7, 2, 1, 4, 1), (8, 2, 0, 4, 1), (8, 2, 1, -1, 1), (8, 2, 1, 4, 0),
                 (8, 2, 1, 1 << 25, 1), (8, 2, 1, 1 << 60, 1)]:
         assert ws(*bad) == 0, bad
-    assert 0 < ws(8, 2, 1, 4, 1) <= ws(8, 2, 64, 4, 1) <= ws(8, 2, 64, 4000, 1)
+    assert ws(8, 2, 1, 4, 1) == 0 and ws(8, 2, 1, 2, 40) == 0       # short sequences are not split
+    assert 0 < ws(8, 2, 1, 40, 1) <= ws(8, 2, 64, 40, 1) <= ws(8, 2, 64, 4000, 1)
+    assert 0 < ws(8, 2, 1, 40, 40) <= ws(8, 2, 64, 40, 40)
     assert ws(1024, 1024, 65535, 1 << 20, 1) < 1 << 26          # bounded by the GPU's size, not by the batch
 
 
