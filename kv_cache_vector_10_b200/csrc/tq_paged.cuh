@@ -47,8 +47,7 @@ struct PagedAttn {
     float *part;                     // split partials: [2 * grid][rows (d + 2)]
     void *rec;                       // [grid] tqpaged::Joint
     unsigned long long *status;
-    int min_tiles;                   // least tiles a CTA takes
-    int item_cost;                   // what beginning an item costs, in tiles
+    int item_cost;                   // what beginning an item costs, in units of its tiles
     int whole_tokens;                // items of at most so many tokens are not cut (by the kernel)
     int whole;                       // none is cut: nothing to join, no workspace
     int device;
@@ -114,46 +113,47 @@ __device__ __forceinline__ int tile_token(const Tiles &t, int i, int TT) {
     return (i < t.ts ? i : t.tw + (i - t.ts)) * TT;
 }
 
-// Chunks of R rows of one kv head of a sequence, and what one costs in tiles.
+// Chunks of R rows of one kv head of a sequence, and what one costs, in units
+// of as many tiles as the kernel takes at a time.
 template <int R>
 __device__ __forceinline__ int chunks_of(const PagedAttn &P, const Seq &s) {
     return (int)(((long long)s.n * P.G + R - 1) / R);
 }
-template <int R, int TT>
-__device__ __forceinline__ int tiles_of(const PagedAttn &P, const Seq &s, int chunk) {
+template <int R, int TT, int UNIT>
+__device__ __forceinline__ int units_of(const PagedAttn &P, const Seq &s, int chunk) {
     const int row0 = chunk * R;
-    return chunk_tiles<TT>(P, s, row0, min(s.n * P.G, row0 + R)).n + P.item_cost;
+    return (chunk_tiles<TT>(P, s, row0, min(s.n * P.G, row0 + R)).n + UNIT - 1) / UNIT + P.item_cost;
 }
 
-// This CTA's share of the call's work, counted in tiles sequence by sequence,
+// This CTA's share of the call's work, counted in units sequence by sequence,
 // kv head by kv head, chunk by chunk: [lo, hi) of the whole, and where `lo`
 // falls.  Every CTA takes the same, so a batch of unlike lengths fills the
 // GPU evenly; a chunk cut by a share's border is joined afterwards.  A chunk
-// counts its tiles and, before them, item_cost for its queries and outputs: a
+// counts its units and, before them, item_cost for its queries and outputs: a
 // border that falls there cuts nothing.  Where items stay whole, one belongs to
 // the share in which it begins.
 struct Share {
     long long lo, hi, quota;
     int b;              // sequence in which lo falls
-    long long into;     // tiles of that sequence before lo
-    long long per_head; // tiles of one kv head of that sequence
+    long long into;     // units of that sequence before lo
+    long long per_head; // units of one kv head of that sequence
 };
 
 // A thread counts a sequence of few chunks by itself; one of many is counted
 // by its warp.  Call with whole warps.
-template <int R, int TT>
-__device__ __forceinline__ long long head_tiles(const PagedAttn &P, const Seq &s) {
+template <int R, int TT, int UNIT>
+__device__ __forceinline__ long long head_units(const PagedAttn &P, const Seq &s) {
     constexpr int FEW = 4;
     const int lane = threadIdx.x & 31, chunks = chunks_of<R>(P, s);
     long long sum = 0;
     if (chunks <= FEW)
-        for (int c = 0; c < chunks; ++c) sum += tiles_of<R, TT>(P, s, c);
+        for (int c = 0; c < chunks; ++c) sum += units_of<R, TT, UNIT>(P, s, c);
     for (uint32_t many = __ballot_sync(0xffffffffu, chunks > FEW); many; many &= many - 1) {
         const int from = __ffs(many) - 1;
         const Seq t{0, __shfl_sync(0xffffffffu, s.n, from), __shfl_sync(0xffffffffu, s.len, from)};
         const int all = chunks_of<R>(P, t);
         long long part = 0;
-        for (int c = lane; c < all; c += 32) part += tiles_of<R, TT>(P, t, c);
+        for (int c = lane; c < all; c += 32) part += units_of<R, TT, UNIT>(P, t, c);
 #pragma unroll
         for (int o = 16; o; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
         if (lane == from) sum = part;
@@ -161,7 +161,7 @@ __device__ __forceinline__ long long head_tiles(const PagedAttn &P, const Seq &s
     return sum;
 }
 
-template <int R, int TT, int THREADS>
+template <int R, int TT, int UNIT, int THREADS>
 __device__ __forceinline__ Share find_share(const PagedAttn &P, Share *s_share, long long *s_sum) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (P.batch + THREADS - 1) / THREADS, b0 = tid * per;
@@ -169,7 +169,7 @@ __device__ __forceinline__ Share find_share(const PagedAttn &P, Share *s_share, 
     long long mine = 0, head = 0;
     for (int i = 0; i < per; ++i) {   // whole warps take the same number of turns
         const Seq s = b0 + i < P.batch ? load_seq(P, b0 + i, bad) : Seq{0, 0, 0};
-        head = head_tiles<R, TT>(P, s);
+        head = head_units<R, TT, UNIT>(P, s);
         mine += head * P.Hkv;
     }
     if (bad) atomicOr(reinterpret_cast<unsigned int *>(P.status + 1), TQ_FLAG_INDEX);
@@ -191,7 +191,7 @@ __device__ __forceinline__ Share find_share(const PagedAttn &P, Share *s_share, 
     long long quota;
     if (total >> 32) quota = (total + gridDim.x - 1) / gridDim.x;
     else quota = ((uint32_t)total + gridDim.x - 1) / gridDim.x;
-    quota = max(quota, (long long)P.min_tiles);
+    quota = max(quota, 1ll);
     const long long lo = min(quota * blockIdx.x, total), hi = min(lo + quota, total);
     const bool here = lo < hi && lo >= first && lo < first + mine;
     if (per == 1) {
@@ -201,7 +201,7 @@ __device__ __forceinline__ Share find_share(const PagedAttn &P, Share *s_share, 
         bool found = false;
         for (int i = 0; i < per; ++i) {
             const Seq s = b0 + i < P.batch ? load_seq(P, b0 + i, bad) : Seq{0, 0, 0};
-            head = head_tiles<R, TT>(P, s);
+            head = head_units<R, TT, UNIT>(P, s);
             if (here && !found && lo < at + head * P.Hkv) {
                 *s_share = Share{lo, hi, quota, b0 + i, lo - at, head};
                 found = true;
@@ -224,11 +224,11 @@ struct Joint {
 // The items (chunk of R rows of one kv head of one sequence) that a share
 // reaches, one after another, and the tiles [i0, i1) of each that are its.
 // Whole warps call begin().
-template <int R, int TT>
+template <int R, int TT, int UNIT>
 struct Walk {
     Seq s;
     Tiles tl;
-    int b, h, row0, row1, i0, i1;
+    int b, h, row0, row1, i0, i1, units;
     long long at, hi;   // work done, end of the share
     int span;           // work of this item in the share
     long long start;    // where the item's work begins
@@ -246,7 +246,7 @@ struct Walk {
         const int lane = threadIdx.x & 31, chunks = chunks_of<R>(P, s);
         int c0 = 0;
         for (; chunks > 1; c0 += 32) {
-            const int mine = c0 + lane < chunks ? tiles_of<R, TT>(P, s, c0 + lane) : 0;
+            const int mine = c0 + lane < chunks ? units_of<R, TT, UNIT>(P, s, c0 + lane) : 0;
             long long sum = mine;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -270,12 +270,14 @@ struct Walk {
     __device__ __forceinline__ void item(const PagedAttn &P, int into) {
         row1 = min(s.n * P.G, row0 + R);
         tl = chunk_tiles<TT>(P, s, row0, row1);
-        const int rest = tl.n + P.item_cost - into;
+        units = (tl.n + UNIT - 1) / UNIT;
+        const int rest = units + P.item_cost - into;
         span = P.whole ? rest : (int)min((long long)rest, hi - at);
-        i0 = max(into - P.item_cost, 0);
-        i1 = max(into + span - P.item_cost, 0);
+        const int u0 = max(into - P.item_cost, 0), u1 = max(into + span - P.item_cost, 0);
+        i0 = u0 * UNIT;
+        i1 = min(u1 * UNIT, tl.n);
         start = at - into;
-        if (i1 == i0) at = hi;   // the border falls before its first tile: the next CTA's
+        if (u1 == u0) at = hi;   // the border falls before its first tile: the next CTA's
     }
     __device__ __forceinline__ void next(const PagedAttn &P) {
         at += span;
@@ -297,7 +299,7 @@ struct Walk {
     // the note on this share's first item
     __device__ __forceinline__ Joint joint(const PagedAttn &P, const Share &sh) const {
         const long long first = start + P.item_cost;   // where its first tile counts
-        return Joint{row0, !more() || begins() ? 0 : row1 - row0, (int)(first / sh.quota), (int)((first + tl.n - 1) / sh.quota), s.q0, h};
+        return Joint{row0, !more() || begins() ? 0 : row1 - row0, (int)(first / sh.quota), (int)((first + units - 1) / sh.quota), s.q0, h};
     }
 };
 
@@ -462,16 +464,16 @@ cudaError_t tq_paged_allow(K kern, int bytes, int regs, int device, std::atomic<
     return e;
 }
 
-// CTAs of a call of at most `items` items of at most `tiles` tiles, and its
+// CTAs of a call of at most `items` items of at most `units` units, and its
 // workspace: notes for the joining kernel, and two parts of R rows a CTA.
 struct PagedGrid {
     int ctas;
     size_t notes, bytes;
 };
 
-inline PagedGrid tq_paged_grid(PagedAttn &P, int64_t items, int64_t tiles, int most_ctas, int R, int D) {
+inline PagedGrid tq_paged_grid(PagedAttn &P, int64_t items, int64_t units, int most_ctas, int R, int D) {
     P.whole = P.max_tokens <= P.whole_tokens;
-    const int64_t bound = P.whole ? items : (items * tiles + P.min_tiles - 1) / P.min_tiles;
+    const int64_t bound = P.whole ? items : items * units;
     PagedGrid g{(int)std::max<int64_t>(1, std::min<int64_t>(most_ctas, bound)), 0, 0};
     if (g.ctas == 1) P.whole = 1;
     if (P.whole) return g;

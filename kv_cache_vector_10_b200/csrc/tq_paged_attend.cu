@@ -17,7 +17,7 @@
 // shares, the first tiles' way from memory, the last's way through the warps,
 // and the join.  4 sequences of 32768 tokens, 8 kv heads, 32 query heads, d =
 // 128 (143 MB): 42 us, 51% of the copy rate; one sequence of 1024 tokens and
-// one kv head: 8.2 us.  Hence:
+// 8 kv heads, not split: 11 us, as long as its host work.  Hence:
 //   * codes go from shared memory into registers as the fragments of
 //     mma.m16n8k16 (tokens or channels as the 16 rows, queries as the 8
 //     columns) and are widened there: no operand is written back to shared
@@ -33,6 +33,7 @@
 //     them across items; those four meet only where an item ends;
 //   * every CTA has the same share of all tiles, whatever the sequences'
 //     lengths; an item cut by a share's border is joined by a second kernel.
+//     Where all are short, none is cut and there is no second kernel.
 // The probabilities are rounded to binary16 (error 2^-12 of each weight,
 // half a rounding step of a binary16 output); queries are taken to binary16
 // after a power-of-two scaling by their largest channel (bfloat16; exact
@@ -170,13 +171,13 @@ __global__ void __launch_bounds__(THREADS, Cfg<D, NT>::CTAS) tq_paged_decode_ker
         tqdev::fence_barrier_init();
     }
     tqdev::grid_dep_trigger();
-    const Share sh = find_share<R, TT, THREADS>(P, &s_share, s_sum);
+    const Share sh = find_share<R, TT, NW, THREADS>(P, &s_share, s_sum);
     if (s_abort || sh.lo >= sh.hi) {
         if (tid == 0 && !P.whole) static_cast<Joint *>(P.rec)[blockIdx.x].rows = 0;
         return;
     }
     bool failed = false;
-    Walk<R, TT> it;
+    Walk<R, TT, NW> it;
     it.begin(P, sh);
     if (warp == NW) {
         // --------------------------------------------- requests, items ahead
@@ -504,11 +505,14 @@ template <int D, int NT>
 tq_status launch_decode(PagedAttn P, int64_t rows, int n_sms, cudaStream_t stream, size_t *need) {
     using C = Cfg<D, NT>;
     constexpr int R = 8 * NT;
-    P.min_tiles = NW;
-    // loading an item's queries, joining its warps' parts and the groups of
-    // four tiles that it does not fill: drafted tokens 21.1 us without, 18.9
-    // with 4; 4 x 32768 tokens 43.3 and 41.7; 256 items of 64 tiles 43.3 and 44.2
-    P.item_cost = 4;
+    // Shares are counted in rounds of a tile for each of the four warps, since
+    // a part of a round takes as long as a whole one (in single tiles: 8 x 4096
+    // tokens of 32 kv heads 45.0 us instead of 43.6, drafted tokens 18.6
+    // instead of 17.1, 4 x 32768 the same, but 32 windows of 1024, short
+    // against a round, 23.6 instead of 24.6).  An item's queries and the join
+    // of its warps' parts take about a round (not counted: drafted tokens 18.6,
+    // 4 x 32768 43.5 instead of 42.2, the others within 1%).
+    P.item_cost = 1;
     // Uncut, a short item saves the second launch and the join: at d = 128 one
     // sequence of 512 tokens takes 7.9 us instead of 9.8, of 1024 10.8 instead
     // of 10.3 (15.1 to 10.9 us with the call's host work), of 2048 16.5 instead
@@ -516,7 +520,7 @@ tq_status launch_decode(PagedAttn P, int64_t rows, int n_sms, cudaStream_t strea
     // 1024 tokens 9.8 and 9.5, at d = 256 512 tokens 12.9 and 12.3.
     P.whole_tokens = 131072 / D;
     const int64_t items = (int64_t)P.batch * P.Hkv * ((rows + R - 1) / R);
-    const PagedGrid grid = tq_paged_grid(P, items, P.max_tokens / C::TT + 1, n_sms * C::CTAS, R, D);
+    const PagedGrid grid = tq_paged_grid(P, items, P.max_tokens / (C::TT * NW) + 1, n_sms * C::CTAS, R, D);
     if (need) {
         *need = grid.bytes;
         return TQ_OK;

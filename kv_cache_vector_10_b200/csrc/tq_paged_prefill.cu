@@ -31,6 +31,7 @@ namespace {
 using namespace tqpaged;
 
 constexpr int PT = 64;                 // tokens of a tile
+constexpr int UNIT = 1;                // tiles that a CTA's share is counted in
 
 template <int D, int NM>
 struct Pre {
@@ -189,7 +190,7 @@ __global__ void __launch_bounds__(Pre<D, NM>::THREADS, 1) tq_paged_prefill_kerne
         s_abort = tqdev::status_aborted(P.status) ? 1 : 0;
         tqdev::fence_barrier_init();
     }
-    const Share sh = find_share<R, PT, C::THREADS>(P, &s_share, s_sum);
+    const Share sh = find_share<R, PT, UNIT, C::THREADS>(P, &s_share, s_sum);
     if (s_abort || sh.lo >= sh.hi) {
         if (tid == 0 && !P.whole) static_cast<Joint *>(P.rec)[blockIdx.x].rows = 0;
         return;
@@ -202,7 +203,7 @@ __global__ void __launch_bounds__(Pre<D, NM>::THREADS, 1) tq_paged_prefill_kerne
     const int lg_part = min(P.lg_page, 6), parts = PT >> lg_part;
     const uint32_t all_parts = (1u << parts) - 1u;
     bool failed = false;
-    Walk<R, PT> it;
+    Walk<R, PT, UNIT> it;
     it.begin(P, sh);
     if (tid == 0 && !P.whole) static_cast<Joint *>(P.rec)[blockIdx.x] = it.joint(P, sh);
 
@@ -575,7 +576,6 @@ __global__ void __launch_bounds__(Pre<D, NM>::THREADS, 1) tq_paged_prefill_kerne
 template <int D, int NM>
 tq_status launch_prefill(PagedAttn P, int64_t rows, int n_sms, cudaStream_t stream, size_t *need) {
     using C = Pre<D, NM>;
-    P.min_tiles = 4;
     // queries into TMEM and outputs out of it take about as long as eight
     // tiles: ragged prompts under a window 182 us without, 120 with 4, 112
     // with 8, 117 with 16; 2048 tokens over 8192 the same within 2%
@@ -585,7 +585,7 @@ tq_status launch_prefill(PagedAttn P, int64_t rows, int n_sms, cudaStream_t stre
     // 46.5, one of 1024 47 instead of 33.5
     P.whole_tokens = 512;
     const int64_t items = (int64_t)P.batch * P.Hkv * ((rows + C::R - 1) / C::R);
-    const PagedGrid grid = tq_paged_grid(P, items, P.max_tokens / PT + 1, n_sms, C::R, D);
+    const PagedGrid grid = tq_paged_grid(P, items, P.max_tokens / (4 * PT) + 1, n_sms, C::R, D);
     if (need) {
         *need = grid.bytes;
         return TQ_OK;
