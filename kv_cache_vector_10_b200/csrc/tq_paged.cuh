@@ -372,6 +372,13 @@ __device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t b
     return r;
 }
 
+// lo, hi += the two halves of h
+__device__ __forceinline__ void add_halves(float &lo, float &hi, uint32_t h) {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+        "add.rn.f32.f16 %0, a, %0;\n\tadd.rn.f32.f16 %1, b, %1;\n\t}"
+        : "+f"(lo), "+f"(hi) : "r"(h));
+}
+
 // A scale as widen() takes it, two of them side by side (w: a scale byte in
 // the low bits of each half).  Everything is 2^-7 of its true size: then
 // 1032 s fits binary16 for every scale, and every value below is still exact,

@@ -118,12 +118,6 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
     return r;
 }
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -331,19 +325,20 @@ __global__ void __launch_bounds__(Pre<D, NM>::THREADS, 1) tq_paged_prefill_kerne
                 const float ref = m_run == -INFINITY ? 0.f : m_run - BIAS;
                 float w[32];
                 const uint64_t mul2 = pack2(mul, mul), ref2 = pack2(-ref, -ref);
-                uint64_t l2[2] = {0, 0};
+                // the sum of the weights as they are rounded: where few tokens
+                // carry a row, their rounding cancels
+                float l[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int c = 0; c < 32; ++c) {
                     float a, b;
                     unpack2(fma2(pack2(x[c >> 4][2 * (c & 15)], x[c >> 4][2 * (c & 15) + 1]), mul2, ref2), a, b);
                     a = exp2_fast(a);
                     b = exp2_fast(b);
-                    l2[c & 1] = add2(l2[c & 1], pack2(a, b));
-                    w[c] = __uint_as_float(h2u(__floats2half2_rn(a, b)));
+                    const uint32_t h = h2u(__floats2half2_rn(a, b));
+                    add_halves(l[2 * (c & 1)], l[2 * (c & 1) + 1], h);
+                    w[c] = __uint_as_float(h);
                 }
-                float l0, l1;
-                unpack2(add2(l2[0], l2[1]), l0, l1);
-                l_run += l0 + l1;
+                l_run += (l[0] + l[1]) + (l[2] + l[3]);
                 tqdev::tmem_st_32x32b_x32(t_s, w);
                 tqdev::tmem_wait_st();
                 tqdev::tc_fence_before();

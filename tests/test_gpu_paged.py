@@ -610,3 +610,33 @@ def test_short_sequences_whole_or_split(d, most):
             out = cache.attention(q, t, lens_t, q_starts=st, max_q_len=most, window=window, sinks=sinks)
             _check(cache, q, table, lens_t, starts, out, window=window, sinks=sinks)
     assert cache.status() == (0, 0)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("most", [1, 60])
+@pytest.mark.parametrize("page_ids", [0, 300])
+def test_equal_values_are_given_back(d, most, page_ids):
+    """Weights are divided by the sum of what they are rounded to, so that
+    values which are the same for every token come back as they are stored:
+    the float32 sums of at most 500 products are off by less than 500 * 2^-22,
+    under half a step of binary16 (2^-11 relative), and a stored value has
+    seven significant bits.  A wider page table: split and joined."""
+    lens, new = [500, 2, 5, 257, 33], [min(n, most) for n in (60, 2, 5, 50, 1)]
+    starts = np.concatenate(([0], np.cumsum(new)))
+    n = sum(lens)
+    g = _gen(d + most)
+    cache = tq.PagedCache(sum((x + 31) // 32 for x in lens), 2, d, page_size=32)
+    table = torch.full((len(lens), max(16, page_ids)), -1, dtype=torch.int32)
+    slots, at = [], 0
+    for b, x in enumerate(lens):
+        pages = (x + 31) // 32
+        table[b, :pages] = torch.arange(at, at + pages)
+        slots.append(at * 32 + torch.arange(x))
+        at += pages
+    k = _randn(g, n, 2, d, dtype=torch.float16) * 2
+    row = _randn(g, 1, 2, d, dtype=torch.float16)
+    stored = cache.write(k, row.expand(n, 2, d).contiguous(), torch.cat(slots).to(DEV), stored=True)[1][0]
+    q = _randn(g, int(starts[-1]), 8, d, dtype=torch.float16)
+    out = cache.attention(q, table.to(DEV), torch.tensor(lens, dtype=torch.int32, device=DEV),
+                          q_starts=torch.tensor(starts, dtype=torch.int32, device=DEV), max_q_len=most)
+    assert torch.equal(out, stored.repeat_interleave(4, 0).expand_as(out))
