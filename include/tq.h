@@ -464,6 +464,8 @@ tq_status tq_paged_read(tq_paged *ctx, const tq_pages *pages, const int64_t *slo
  *   t <= p, and, where window > 0, only t > p - window or t < sinks
  * (a sliding window and a few first tokens that stay visible).
  *   out = sum_t softmax_t(scale q . k_t) v_t,  zeros where nothing is seen.
+ * A row of q with a NaN, or with an infinity that makes a score NaN or +inf,
+ * gives a row of NaN (where it sees something) and changes no other row.
  *  q, out     : device, binary16 or bfloat16 (`dtype`; the scores and sums are
  *               float32, the weights binary16, the products exact), element
  *               (row i, head j, channel c) at i * stride_?t + j * stride_?h + c;

@@ -423,8 +423,8 @@ __global__ void __launch_bounds__(THREADS, Cfg<D, NT>::CTAS) tq_paged_decode_ker
 #pragma unroll
             for (int w = 1; w < NW; ++w) m = fmaxf(m, sm[w][r]);
 #pragma unroll
-            for (int w = 0; w < NW; ++w)
-                if (sm[w][r] != -INFINITY) l += sl[w][r] * exp2_fast(sm[w][r] - m);
+            for (int w = 0; w < NW; ++w)   // (a part that saw nothing adds nothing; one of NaN alone has no maximum, but a sum)
+                if (sm[w][r] != -INFINITY || sl[w][r] != 0.f) l += sl[w][r] * exp2_fast(sm[w][r] - m);
             if (direct) {
                 if (it.row0 + r < it.row1) {
                     const float inv = l != 0.f ? 1.f / l : 0.f;
@@ -471,7 +471,7 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) tq_paged_join_kernel(const __
         float m = -INFINITY, l = 0.f;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
         auto add = [&](float mk, float lk, const float4 &y) {
-            if (mk == -INFINITY) return;
+            if (mk == -INFINITY && lk == 0.f) return;   // saw nothing; where all scores are NaN, l is NaN and the row becomes it
             const float to = fmaxf(m, mk), f = m == -INFINITY ? 0.f : exp2_fast(m - to), g = exp2_fast(mk - to);
             m = to;
             l = l * f + lk * g;
@@ -484,7 +484,7 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) tq_paged_join_kernel(const __
 #pragma unroll
             for (int b = 0; b < B; ++b) {
                 const int k = k0 + b * groups;
-                mk[b] = -INFINITY;
+                mk[b] = -INFINITY, lk[b] = 0.f;
                 if (k < n) {
                     const float *p = P.part + ((int64_t)(J.first + k) * 2 + (k == 0 ? 1 : 0)) * size;
                     mk[b] = __ldcg(p + (int64_t)R * D + r);

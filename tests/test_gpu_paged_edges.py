@@ -1,0 +1,41 @@
+"""The paged 4-bit cache on the GPU: calls at the edges of what its
+documentation allows, and calls that it refuses."""
+import numpy as np
+import pytest
+import torch
+
+from test_gpu_paged import DEV, _check, _gen, _pool, _randn, tq
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------ queries that are not finite
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("most", [1, 60])
+def test_queries_that_are_not_finite_where_sequences_are_split(dtype, d, most):
+    """A NaN in a query, or an infinity (some score is then NaN or +inf), makes
+    its row NaN whether the sequence is split or not, and no other row; a row
+    that sees nothing is zeros whatever its query."""
+    lens, new = [5000, 20, 300], [most, min(most, 59), 1]
+    if most > 1:
+        new[1] = 33                              # 13 queries before the first token
+    starts = np.concatenate(([0], np.cumsum(new)))
+    cache, table, lens_t, g = _pool(lens, 2, d, 16, seed=d + most, dtype=dtype)
+    assert cache.workspace_bytes(8, 3, table.shape[1], most) > 0
+    q = _randn(g, int(starts[-1]), 8, d, dtype=dtype)
+    st = torch.tensor(starts, dtype=torch.int32, device=DEV)
+    good = cache.attention(q, table, lens_t, q_starts=st, max_q_len=most)
+    bad = q.clone()
+    hit = torch.zeros(q.shape[:2], dtype=torch.bool, device=DEV)
+    for i, (row, head) in enumerate([(0, 0), (0, 3), (0, 5), (new[0] - 1, 6), (int(starts[2]), 1), (int(starts[2]) - 1, 2)]):
+        bad[row, head, (7 * i) % d] = (float("nan"), float("inf"), -float("inf"))[i % 3]
+        hit[row, head] = True
+    if most > 1:
+        bad[new[0], 4, 3] = bad[new[0] + 5, 4, 9] = float("nan")     # these see nothing
+    out = cache.attention(bad, table, lens_t, q_starts=st, max_q_len=most)
+    assert out[hit].isnan().all()
+    assert torch.equal(out[~hit], good[~hit])
+    if most > 1:
+        assert not out[new[0]:new[0] + 13].any()
