@@ -474,7 +474,9 @@ tq_status tq_paged_read(tq_paged *ctx, const tq_pages *pages, const int64_t *slo
  *               not overlap q.  Rows of `out` outside every sequence are left
  *               as they were.
  *  page_table : device int32, table_stride >= max_pages entries a sequence;
- *               entries past a sequence's length are not read.
+ *               entries of pages of which no query sees a token (past the
+ *               length, or between the sinks and the first query's window)
+ *               are not read.
  *  seq_lens   : device int32 [batch].
  *  q_starts   : device int32 [batch + 1], or NULL: one query per sequence
  *               (total_q == batch).

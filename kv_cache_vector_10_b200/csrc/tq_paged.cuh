@@ -109,6 +109,13 @@ __device__ __forceinline__ Tiles chunk_tiles(const PagedAttn &P, const Seq &s, i
     return t;
 }
 
+// Whether some query of the chunk sees a token of [tok, tok + n): the windows of
+// consecutive positions leave no gap.  Pages of other tokens are not looked up:
+// a serving loop may have given them back.
+__device__ __forceinline__ bool any_seen(const PagedAttn &P, const Tiles &t, int tok, int n) {
+    return tok <= t.p_hi && (P.window <= 0 || tok + n - 1 > t.p_lo - P.window || tok < P.sinks);
+}
+
 __device__ __forceinline__ int tile_token(const Tiles &t, int i, int TT) {
     return (i < t.ts ? i : t.tw + (i - t.ts)) * TT;
 }
@@ -319,10 +326,11 @@ struct TileLoad {
         tile = lane / parts;
         part = lane % parts;
     }
-    // the token at which this lane's part begins, tiles from i on of [.., i1); -1 for none
-    __device__ __forceinline__ int token(const Tiles &t, int i, int i1, int len) const {
+    // the token at which this lane's part begins, tiles from i on of [.., i1);
+    // -1 for none, or where no query of the chunk sees it
+    __device__ __forceinline__ int token(const PagedAttn &P, const Tiles &t, int i, int i1) const {
         const int tok = tile_token(t, i + tile, TT) + (part << lg);
-        return tile < TILES && i + tile < i1 && tok < len ? tok : -1;
+        return tile < TILES && i + tile < i1 && any_seen(P, t, tok, 1 << lg) ? tok : -1;
     }
     static __device__ __forceinline__ int fetch(const PagedAttn &P, int b, int tok) {
         return tok < 0 ? -1 : __ldg(P.table + (int64_t)b * P.table_stride + (tok >> P.lg_page));

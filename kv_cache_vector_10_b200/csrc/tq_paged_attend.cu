@@ -189,9 +189,9 @@ __global__ void __launch_bounds__(THREADS, Cfg<D, NT>::CTAS) tq_paged_decode_ker
         const typename C::Load load(P, lane);
         int n = 0;
         for (; it.more() && !failed; it.next(P)) {
-            int tok = load.token(it.tl, it.i0, it.i1, it.s.len), page = C::Load::fetch(P, it.b, tok);
+            int tok = load.token(P, it.tl, it.i0, it.i1), page = C::Load::fetch(P, it.b, tok);
             for (int i = it.i0; i < it.i1; i += NW, ++n) {
-                const int st = n % NST, tok2 = load.token(it.tl, i + NW, it.i1, it.s.len), page2 = C::Load::fetch(P, it.b, tok2);
+                const int st = n % NST, tok2 = load.token(P, it.tl, i + NW, it.i1), page2 = C::Load::fetch(P, it.b, tok2);
                 if (n >= NST && !__all_sync(0xffffffffu, tqdev::mbar_wait_bounded(&freed[st], (uint32_t)(n / NST - 1) & 1u))) {
                     failed = true;
                     break;

@@ -454,9 +454,9 @@ __global__ void __launch_bounds__(Pre<D, NM>::THREADS, 1) tq_paged_prefill_kerne
         const typename C::Load load(P, lane);
         int n = 0;
         for (; it.more() && !failed; it.next(P)) {
-            int tok = load.token(it.tl, it.i0, it.i1, it.s.len), page = C::Load::fetch(P, it.b, tok);
+            int tok = load.token(P, it.tl, it.i0, it.i1), page = C::Load::fetch(P, it.b, tok);
             for (int i = it.i0; i < it.i1; ++i, ++n) {
-                const int cs = n % NC, tok2 = load.token(it.tl, i + 1, it.i1, it.s.len), page2 = C::Load::fetch(P, it.b, tok2);
+                const int cs = n % NC, tok2 = load.token(P, it.tl, i + 1, it.i1), page2 = C::Load::fetch(P, it.b, tok2);
                 if (n >= NC && !wait_warp(&bars.codes_free[cs], (uint32_t)(n / NC - 1) & 1u)) {
                     failed = true;
                     break;

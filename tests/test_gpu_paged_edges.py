@@ -39,3 +39,42 @@ def test_queries_that_are_not_finite_where_sequences_are_split(dtype, d, most):
     assert torch.equal(out[~hit], good[~hit])
     if most > 1:
         assert not out[new[0]:new[0] + 13].any()
+
+
+# -------------------------------------------------- what no query sees
+
+def _visible(lens, new, width, page, window, sinks):
+    """Of each sequence: which of `width` pages hold a token that some query
+    sees, and which tokens are seen."""
+    pages, tokens = torch.zeros(len(lens), width, dtype=torch.bool), []
+    for b, (n, m) in enumerate(zip(lens, new)):
+        t = torch.arange(n)
+        see = ((t > n - m - window) | (t < sinks)) if m else torch.zeros(n, dtype=torch.bool)
+        pages[b, (t[see] // page).unique()] = True
+        tokens.append(see)
+    return pages, tokens
+
+
+WINDOWS = [(1, 0), (100, 4), (64, 0), (130, 70), (17, 1000)]
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("page", [16, 64, 256])
+@pytest.mark.parametrize("most", [1, 5, 70])
+@pytest.mark.parametrize("window,sinks", WINDOWS)
+def test_pages_that_no_query_sees_may_be_freed(d, page, most, window, sinks):
+    """A serving loop gives back the pages behind the window: their entries
+    are not looked up and nothing is flagged."""
+    lens = [900, 40, 513, 0, 300, 2600]
+    new = [min(n, most) for n in lens]
+    starts = torch.tensor(np.concatenate(([0], np.cumsum(new))), dtype=torch.int32, device=DEV)
+    cache, table, lens_t, g = _pool(lens, 2, d, page, seed=d + page + most)
+    q = _randn(g, sum(new), 4, d, dtype=torch.float16)
+    kw = dict(q_starts=starts, max_q_len=most, window=window, sinks=sinks)
+    good = cache.attention(q, table, lens_t, **kw)
+    _check(cache, q, table, lens_t, starts.cpu().numpy(), good, window=window, sinks=sinks)
+    keep, _ = _visible(lens, new, table.shape[1], page, window, sinks)
+    for entry in (-1, 1 << 30):
+        out = cache.attention(q, torch.where(keep.to(DEV), table, entry), lens_t, **kw)
+        assert torch.equal(out, good)
+    assert cache.status() == (0, 0)
