@@ -489,7 +489,7 @@ tq_status tq_paged_read(tq_paged *ctx, const tq_pages *pages, const int64_t *slo
  *               is 0 (and the pointer may be NULL) where max_pages allows only
  *               short sequences, which are not split, and on invalid
  *               arguments.
- * Tokens past a sequence's length may hold anything.  A length outside
+ * Tokens that no query sees may hold anything.  A length outside
  * [0, max_pages * page_size], a query start outside [0, total_q] or a
  * decreasing one is held to those bounds, tokens of a page number outside the
  * pool are not seen, and each sets error flag bit 1 in the status word.

@@ -336,13 +336,15 @@ struct TileLoad {
         return tok < 0 ? -1 : __ldg(P.table + (int64_t)b * P.table_stride + (tok >> P.lg_page));
     }
     // Requests the tiles into `dst`, their parts that are there into *valid
-    // (a bit each, tile by tile) before that.
+    // (a bit each, tile by tile) before that; note(those) by whole warps.
+    template <typename Note>
     __device__ __forceinline__ void request(const PagedAttn &P, int tok, int page, int h, int lane, uint8_t *dst,
-                                            volatile uint32_t *valid, uint64_t *bar) const {
+                                            volatile uint32_t *valid, uint64_t *bar, Note note) const {
         const bool ok = tok >= 0 && page >= 0 && page < P.n_pages;
         if (tok >= 0 && !ok) atomicOr(reinterpret_cast<unsigned int *>(P.status + 1), TQ_FLAG_INDEX);
         const uint32_t got = __ballot_sync(0xffffffffu, ok);
         const uint32_t codes = (uint32_t)(D / 2) << lg, scales = (uint32_t)(D / 32) << lg;
+        note(got);
         if (lane == 0) {
             *valid = got;
             tqdev::mbar_expect_tx(bar, (uint32_t)__popc(got) * 2u * (codes + scales));

@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(Pre<D, NM>::THREADS, 1) tq_paged_prefill_kerne
     __shared__ __align__(8) PreBars bars;
     __shared__ Share s_share;
     __shared__ long long s_sum[C::THREADS / 32];
-    __shared__ uint32_t s_tmem, s_valid[16];   // s_valid: which parts of a tile were there, 16 tiles back
+    __shared__ uint32_t s_tmem, s_valid[16], s_seen[16][2];   // which parts of a tile were there, which rows are seen: 16 tiles back
     __shared__ int s_abort;
 
     const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
@@ -419,15 +419,13 @@ __global__ void __launch_bounds__(Pre<D, NM>::THREADS, 1) tq_paged_prefill_kerne
                 }
                 const uint8_t *codes = sm + C::OFF_C + cs * C::Load::STAGE + kv * C::Load::SIDE;
                 uint8_t *tile = sm + (kv ? C::OFF_V : 0) + b * C::TILE;
-                const uint32_t got = *reinterpret_cast<volatile uint32_t *>(&s_valid[n & 15]);
-                const int T0 = tile_token(it.tl, i, PT);
+                // this warp's rows that some query sees, a bit each; the others may hold anything
+                const uint32_t seen = *reinterpret_cast<volatile uint32_t *>(&s_seen[n & 15][ROWS * e / 32]) >> (ROWS * e % 32);
 #pragma unroll
                 for (int g = 0; g < ROWS; g += STEP) {
                     const int tr = ROWS * e + g + lane / GROUPS;   // this lane's token
                     const uint8_t *src = codes + C::Load::codes_at(tr, lg_part) + 16 * grp;
-                    // a row that holds no token of this sequence may hold anything
-                    const bool there = T0 + tr < it.s.len && ((got >> (tr >> lg_part)) & 1u);
-                    const Scale2 sc = scale2((there ? codes[C::Load::scales_at(tr, lg_part) + grp] : 0u) * 0x00010001u);
+                    const Scale2 sc = scale2(((seen >> (g + lane / GROUPS)) & 1u ? codes[C::Load::scales_at(tr, lg_part) + grp] : 0u) * 0x00010001u);
                     uint8_t *dst = tile + (grp >> 1) * C::KX + tr * 128;
                     const int first = D == 256 ? (grp >> 1) + tr : D == 128 ? 2 * (grp >> 1) + (tr >> 1) : tr >> 2;
 #pragma unroll
@@ -461,7 +459,18 @@ __global__ void __launch_bounds__(Pre<D, NM>::THREADS, 1) tq_paged_prefill_kerne
                     failed = true;
                     break;
                 }
-                load.request(P, tok, page, it.h, lane, sm + C::OFF_C + cs * C::Load::STAGE, &s_valid[n & 15], &bars.codes_full[cs]);
+                // (the rows that are seen are found here, once a tile and off
+                // the widening warps' way, where it took windowed prompts of
+                // d = 256 119 us instead of 115)
+                load.request(P, tok, page, it.h, lane, sm + C::OFF_C + cs * C::Load::STAGE, &s_valid[n & 15], &bars.codes_full[cs],
+                             [&](uint32_t got) {
+#pragma unroll
+                                 for (int x = 0; x < 2; ++x) {
+                                     const int row = 32 * x + lane;
+                                     const uint32_t rows = __ballot_sync(0xffffffffu, any_seen(P, it.tl, tile_token(it.tl, i, PT) + row, 1) && ((got >> (row >> lg_part)) & 1u));
+                                     if (lane == 0) *reinterpret_cast<volatile uint32_t *>(&s_seen[n & 15][x]) = rows;
+                                 }
+                             });
                 tok = tok2;
                 page = page2;
             }

@@ -78,3 +78,30 @@ def test_pages_that_no_query_sees_may_be_freed(d, page, most, window, sinks):
         out = cache.attention(q, torch.where(keep.to(DEV), table, entry), lens_t, **kw)
         assert torch.equal(out, good)
     assert cache.status() == (0, 0)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("page", [16, 64, 256])
+@pytest.mark.parametrize("most", [1, 5, 70])
+@pytest.mark.parametrize("window,sinks", WINDOWS)
+def test_rows_that_no_query_sees_may_hold_anything(d, page, most, window, sinks):
+    """Rows outside every query's window and sinks, in pages that are partly
+    seen too: their scale bytes may stand for NaN or infinity."""
+    lens = [900, 40, 513, 0, 300, 2600]
+    new = [min(n, most) for n in lens]
+    starts = torch.tensor(np.concatenate(([0], np.cumsum(new))), dtype=torch.int32, device=DEV)
+    cache, table, lens_t, g = _pool(lens, 2, d, page, seed=d + page + most)
+    q = _randn(g, sum(new), 4, d, dtype=torch.float16)
+    kw = dict(q_starts=starts, max_q_len=most, window=window, sinks=sinks)
+    good = cache.attention(q, table, lens_t, **kw)
+    seen = torch.zeros(cache.n_pages * page, dtype=torch.bool)
+    for b, see in enumerate(_visible(lens, new, table.shape[1], page, window, sinks)[1]):
+        t = torch.arange(lens[b])[see]
+        seen[table[b].cpu()[t // page].long() * page + t % page] = True
+    hide = ~seen.view(cache.n_pages, page).to(DEV)
+    for byte in (0xFF, 0xF8):                        # scales of NaN and of infinity
+        for pool in (cache.k, cache.v):
+            scales = pool[..., page * d // 2:].view(cache.n_pages, 2, page, d // 32)
+            scales.copy_(torch.where(hide[:, None, :, None], byte, scales))
+        assert torch.equal(cache.attention(q, table, lens_t, **kw), good)
+    assert cache.status() == (0, 0)
