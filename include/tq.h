@@ -398,7 +398,8 @@ tq_status tq_reset_status(tq_ctx *ctx, void *stream);
  * |x - c s| <= s / 2 while max|x| <= 57600, beyond which values saturate.
  * c s is exact in binary16, bfloat16 and float32.  A row (one head vector)
  * with a value that is not finite is kept as zeros and counted in the status
- * word.  A page of one kv head is page_size * (d/2 + d/32) bytes: the codes
+ * word (rows that are not kept, padding among them, are not counted).  A page
+ * of one kv head is page_size * (d/2 + d/32) bytes: the codes
  * [page_size][d/2], c + 8 of channel j in nibble j % 2 of byte j / 2, then
  * the scale bytes [page_size][d/32].
  *

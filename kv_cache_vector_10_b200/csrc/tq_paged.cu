@@ -206,7 +206,7 @@ __device__ __forceinline__ void quantise_store(uint32_t (&x)[Plain<T>::W], bool 
 #pragma unroll
         for (int i = 0; i < Plain<T>::W; ++i) x[i] = 0;
         m = 0;
-        if (live && j == 0) ++bad_rows;
+        if (kept && j == 0) ++bad_rows;   // (padding may hold anything)
     }
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
     float amax;

@@ -105,3 +105,20 @@ def test_rows_that_no_query_sees_may_hold_anything(d, page, most, window, sinks)
             scales.copy_(torch.where(hide[:, None, :, None], byte, scales))
         assert torch.equal(cache.attention(q, table, lens_t, **kw), good)
     assert cache.status() == (0, 0)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16])
+def test_padding_rows_are_not_counted(dtype):
+    """Rows without a place in the cache (padding, slots past the pool) may
+    hold anything; only rows that are kept are counted as not finite."""
+    cache = tq.PagedCache(2, 2, 64, page_size=16)
+    x = _randn(_gen(1), 6, 2, 64, dtype=dtype)
+    x[1] = float("nan")
+    x[2, 0, 3] = float("inf")
+    x[4] = -float("inf")
+    x[5, 1, 0] = float("nan")
+    slots = torch.tensor([0, -1, -7, 3, 32, 5], device=DEV)
+    ks, vs = cache.write(x, x, slots, stored=True)
+    assert cache.status() == (2, 2)                  # the row (5, 1) of keys and of values; a slot past the pool
+    assert not ks[1].any() and not ks[2, 0].any() and ks[2, 1].any() and not vs[4].any() and not ks[5, 1].any()
+    assert not cache.read(torch.tensor([5], device=DEV))[0][0, 1].any()
