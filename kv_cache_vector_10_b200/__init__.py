@@ -630,7 +630,7 @@ class PagedCache:
         and the end (None: one query per sequence); max_q_len: the most
         queries of a sequence, as a hint (default their mean);
         window: 0, or how many tokens back a query sees besides the first
-        `sinks`; scale: default 1/sqrt(head_dim).  Returns `out` (like q;
+        `sinks`; scale: positive (default 1/sqrt(head_dim)).  Returns `out` (like q;
         rows of no sequence are not written)."""
         if not self._here(stream):
             return self._elsewhere(stream, self.attention, q, page_table, seq_lens, q_starts, max_q_len, window, sinks,
@@ -638,6 +638,10 @@ class PagedCache:
         torch, dev, i32 = self._torch, self._index, self._torch.int32
         code = self._halves.get(q.dtype)
         if code is None or q.dim() != 3 or page_table.dim() != 2 or q.shape[2] != self.head_dim:
+            raise TQError(8, "PagedCache.attention")
+        if scale is None:
+            scale = 0.0                                      # the library's default
+        elif not ctypes.c_float(scale).value > 0:            # (0 would be taken for it)
             raise TQError(8, "PagedCache.attention")
         total, heads, _ = q.shape
         batch, pages = page_table.shape
@@ -682,7 +686,7 @@ class PagedCache:
         sot, soh, _ = out.stride()
         err = _lib.tq_paged_attention(
             self.ctx, self._pages_ref, q.data_ptr(), code, total, heads, sqt, sqh, page_table.data_ptr(), srow, pages,
-            seq_lens.data_ptr(), starts, batch, most, window, sinks, scale or 0.0, out.data_ptr(), sot, soh,
+            seq_lens.data_ptr(), starts, batch, most, window, sinks, scale, out.data_ptr(), sot, soh,
             None if workspace is None else workspace.data_ptr(), need, torch._C._cuda_getCurrentRawStream(dev))
         if err:
             raise TQError(err, "tq_paged_attention")

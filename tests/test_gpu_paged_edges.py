@@ -122,3 +122,15 @@ def test_padding_rows_are_not_counted(dtype):
     assert cache.status() == (2, 2)                  # the row (5, 1) of keys and of values; a slot past the pool
     assert not ks[1].any() and not ks[2, 0].any() and ks[2, 1].any() and not vs[4].any() and not ks[5, 1].any()
     assert not cache.read(torch.tensor([5], device=DEV))[0][0, 1].any()
+
+
+# ------------------------------------------------------- arguments
+
+@pytest.mark.parametrize("scale", [0.0, -0.0, 0, 1e-60, -1e-60, float("inf"), 1e60, float("nan")])
+def test_scales_that_are_not_positive_float32_are_refused(scale):
+    """Zero among them: it is not the default."""
+    cache, table, lens_t, g = _pool([40, 30], 2, 64, 16, seed=1)
+    q = _randn(g, 2, 4, 64, dtype=torch.float16)
+    with pytest.raises(tq.TQError, match="DIM_MISMATCH"):
+        cache.attention(q, table, lens_t, scale=scale)
+    assert torch.equal(cache.attention(q, table, lens_t, scale=64 ** -0.5), cache.attention(q, table, lens_t))
