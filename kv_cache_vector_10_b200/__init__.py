@@ -466,6 +466,9 @@ class KvCache:
         self._len = 0
 
 
+_INT_MAX = 2 ** 31 - 1                                       # ctypes takes a C int modulo 2^32
+
+
 class PagedCache:
     """A paged cache held in 4 bits (include/tq.h, "A paged cache held in 4
     bits"): a pool of pages shared by many sequences, written with
@@ -483,6 +486,8 @@ class PagedCache:
         self.ctx = None
         if n_pages <= 0 or n_kv_heads <= 0:
             raise TQError(7, "PagedCache")                   # TQ_ERR_EMPTY
+        if max(n_pages, n_kv_heads, head_dim, page_size) > _INT_MAX:
+            raise TQError(13, "PagedCache")                  # TQ_ERR_LIMIT
         device = torch.device(device)
         if device.type != "cuda":
             raise TQError(12, "PagedCache")                  # TQ_ERR_DEVICE
@@ -619,6 +624,8 @@ class PagedCache:
         return kh, vh
 
     def workspace_bytes(self, n_q_heads: int, batch: int, max_pages: int, max_q_len: int = 1) -> int:
+        if max(n_q_heads, batch, max_pages, max_q_len) > _INT_MAX:
+            raise TQError(13, "PagedCache.workspace_bytes")
         return _lib.tq_paged_workspace_bytes(self.ctx, n_q_heads, self.n_kv_heads, batch, max_pages, max_q_len)
 
     def attention(self, q, page_table, seq_lens, q_starts=None, max_q_len=None, window: int = 0, sinks: int = 0,
@@ -658,6 +665,9 @@ class PagedCache:
             q_starts = q_starts.contiguous()
             starts = q_starts.data_ptr()
         most = max_q_len or (1 if q_starts is None or not batch else max(-(-total // batch), 1))
+        if (not -_INT_MAX <= window <= _INT_MAX or not -_INT_MAX <= sinks <= _INT_MAX or not -_INT_MAX <= most <= _INT_MAX
+                or heads > _INT_MAX or batch > _INT_MAX):
+            raise TQError(13, "PagedCache.attention")        # TQ_ERR_LIMIT
         q, seq_lens = self._rows(q), seq_lens.contiguous()
         srow, scol = page_table.stride()
         if scol != 1 or srow < pages:

@@ -134,3 +134,19 @@ def test_scales_that_are_not_positive_float32_are_refused(scale):
     with pytest.raises(tq.TQError, match="DIM_MISMATCH"):
         cache.attention(q, table, lens_t, scale=scale)
     assert torch.equal(cache.attention(q, table, lens_t, scale=64 ** -0.5), cache.attention(q, table, lens_t))
+
+
+@pytest.mark.parametrize("kw", [dict(window=(1 << 32) + 5), dict(window=1 << 32), dict(sinks=1 << 31, window=4),
+                                dict(sinks=(1 << 32) + 2, window=4), dict(max_q_len=(1 << 32) + 1), dict(max_q_len=1 << 31),
+                                dict(window=-(1 << 32) + 4), dict(sinks=-(1 << 32) + 4, window=4), dict(max_q_len=-(1 << 32) + 1)])
+def test_numbers_beyond_32_bits_are_refused(kw):
+    """They are not taken modulo 2^32."""
+    cache, table, lens_t, g = _pool([40, 30], 2, 64, 16, seed=1)
+    with pytest.raises(tq.TQError, match="LIMIT"):
+        cache.attention(_randn(g, 2, 4, 64, dtype=torch.float16), table, lens_t, **kw)
+    for args in [(1 << 32, 1, 1, 1), (4, (1 << 32) + 1, 100, 1), (4, 1, 1 << 31, 1), (4, 1, 100, (1 << 32) + 1)]:
+        with pytest.raises(tq.TQError, match="LIMIT"):
+            cache.workspace_bytes(*args)
+    for args in [(4, 8, 64, (1 << 32) + 64), (4, 8, (1 << 32) + 64, 64), (4, (1 << 32) + 8, 64, 64)]:
+        with pytest.raises(tq.TQError, match="LIMIT"):
+            tq.PagedCache(*args)
