@@ -690,6 +690,8 @@ class PagedCache:
                 workspace = q.new_empty(need, dtype=torch.uint8)
         elif workspace.get_device() != dev:
             raise TQError(12, "PagedCache.attention")
+        elif not workspace.is_contiguous():                  # its bytes would not be where they are counted
+            raise TQError(9, "PagedCache.attention")         # TQ_ERR_WORKSPACE
         else:
             need = workspace.numel() * workspace.element_size()
         sqt, sqh, _ = q.stride()

@@ -150,3 +150,18 @@ def test_numbers_beyond_32_bits_are_refused(kw):
     for args in [(4, 8, 64, (1 << 32) + 64), (4, 8, (1 << 32) + 64, 64), (4, (1 << 32) + 8, 64, 64)]:
         with pytest.raises(tq.TQError, match="LIMIT"):
             tq.PagedCache(*args)
+
+
+def test_workspaces_that_are_not_contiguous_are_refused():
+    """An expanded tensor has fewer bytes than elements, a strided one has
+    others between them."""
+    cache, table, lens_t, g = _pool([4000], 1, 64, 16, seed=2)
+    q = _randn(g, 1, 2, 64, dtype=torch.float16)
+    need = cache.workspace_bytes(2, 1, table.shape[1])
+    assert need > 0
+    for ws in (torch.empty(1, dtype=torch.uint8, device=DEV).expand(need), torch.empty(2 * need, dtype=torch.uint8, device=DEV)[::2],
+               torch.empty(64, dtype=torch.float32, device=DEV).expand(need, 64)):
+        with pytest.raises(tq.TQError, match="WORKSPACE"):
+            cache.attention(q, table, lens_t, workspace=ws)
+    ws = torch.empty(need // 4 + 1, dtype=torch.float32, device=DEV)         # any type will do
+    assert torch.equal(cache.attention(q, table, lens_t, workspace=ws), cache.attention(q, table, lens_t))
