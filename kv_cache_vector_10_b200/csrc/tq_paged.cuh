@@ -490,7 +490,7 @@ struct PagedGrid {
 
 inline PagedGrid tq_paged_grid(PagedAttn &P, int64_t items, int64_t units, int most_ctas, int R, int D) {
     P.whole = P.max_tokens <= P.whole_tokens;
-    const int64_t bound = P.whole ? items : items * units;
+    const int64_t bound = P.whole || items >= most_ctas ? items : items * units;   // (at the limits the product passes 2^63)
     PagedGrid g{(int)std::max<int64_t>(1, std::min<int64_t>(most_ctas, bound)), 0, 0};
     if (g.ctas == 1) P.whole = 1;
     if (P.whole) return g;
