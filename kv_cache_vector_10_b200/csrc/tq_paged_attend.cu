@@ -530,12 +530,20 @@ tq_status launch_decode(PagedAttn P, int64_t rows, int n_sms, cudaStream_t strea
     // of its warps' parts take about a round (not counted: drafted tokens 18.6,
     // 4 x 32768 43.5 instead of 42.2, the others within 1%).
     P.item_cost = 1;
-    // Uncut, a short item saves the second launch and the join: at d = 128 one
-    // sequence of 512 tokens takes 7.9 us instead of 9.8, of 1024 10.8 instead
-    // of 10.3 (15.1 to 10.9 us with the call's host work), of 2048 16.5 instead
-    // of 10.8; 32 sequences of 1024 tokens 14.9 instead of 19.3.  At d = 64
-    // 1024 tokens 9.8 and 9.5, at d = 256 512 tokens 12.9 and 12.3.
-    P.whole_tokens = 131072 / D;
+    // Uncut, a short item saves the second launch and the join; cut, its rounds
+    // run side by side.  Kernel times in us, cut and whole, four query heads a
+    // kv head, by tokens (rounds) and items (sequences times kv heads):
+    //              d = 64             d = 128            d = 256
+    //   rounds   8 items  64 items   8 items  64 items   8 items  64 items
+    //     1      7.1  5.4  7.4  5.8   7.8  6.0  8.2  6.5   9.9  8.2 10.1  8.7
+    //     2      8.0  6.6  8.8  7.0   8.8  7.4  9.9  8.0  11.5  9.9 13.8 10.3
+    //     4      8.2  8.8  9.7  9.2   8.9 10.3 12.0 10.7  11.1 12.9 15.8 13.4
+    //     8      8.4 13.5 11.9 14.0   9.2 15.8 13.0 16.4  11.4 19.3 16.5 19.7
+    // and a call that is not replayed from a graph takes 15.8 cut, 11.3 to 13.4
+    // whole up to four rounds, 13.8 to 20.2 at eight.  So: whole up to four
+    // rounds, where a replayed step of few items loses up to 2.3 us (at four
+    // rounds) and every other call gains 1 to 4.5.
+    P.whole_tokens = 4 * NW * C::TT;
     const int64_t items = (int64_t)P.batch * P.Hkv * ((rows + R - 1) / R);
     const PagedGrid grid = tq_paged_grid(P, items, P.max_tokens / (C::TT * NW) + 1, n_sms * C::CTAS, R, D);
     if (need) {

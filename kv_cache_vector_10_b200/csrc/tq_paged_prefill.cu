@@ -584,9 +584,11 @@ tq_status launch_prefill(PagedAttn P, int64_t rows, int n_sms, cudaStream_t stre
     // tiles: ragged prompts under a window 182 us without, 120 with 4, 112
     // with 8, 117 with 16; 2048 tokens over 8192 the same within 2%
     P.item_cost = 8;
-    // uncut: a prompt of 64 tokens (32 query heads on 8, d = 128) 13.4 us
-    // instead of 22.6, one of 512 29.0 either way, four of 512 39 instead of
-    // 46.5, one of 1024 47 instead of 33.5
+    // uncut, whole prompts, 32 query heads on 8, kernel times cut and whole: at
+    // d = 128 one of 64 tokens 14.0 and 12.4 us, of 128 16.4 and 14.2, of 512
+    // 28.4 and 20.9, of 1024 39.2 and 30.6, eight of 512 72.8 and 63.4; at d =
+    // 256 one of 512 37.7 and 22.1, of 1024 57.7 and 55.9; on a single kv head,
+    // d = 128, one of 512 21.2 and 20.1, of 1024 23.0 and 28.9: the bound
     P.whole_tokens = 512;
     const int64_t items = (int64_t)P.batch * P.Hkv * ((rows + C::R - 1) / C::R);
     const PagedGrid grid = tq_paged_grid(P, items, P.max_tokens / (4 * PT) + 1, n_sms, C::R, D);
