@@ -500,6 +500,7 @@ class PagedCache:
         self.page_bytes = _lib.tq_paged_page_bytes(self.ctx)
         self.k = torch.zeros(n_pages, n_kv_heads, self.page_bytes, dtype=torch.uint8, device=self.device)
         self.v = torch.zeros_like(self.k)
+        torch.cuda.current_stream(self.device).synchronize()         # the first call may be on any stream
         self._prepare()
 
     def _prepare(self):

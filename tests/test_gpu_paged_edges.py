@@ -165,3 +165,21 @@ def test_workspaces_that_are_not_contiguous_are_refused():
             cache.attention(q, table, lens_t, workspace=ws)
     ws = torch.empty(need // 4 + 1, dtype=torch.float32, device=DEV)         # any type will do
     assert torch.equal(cache.attention(q, table, lens_t, workspace=ws), cache.attention(q, table, lens_t))
+
+
+def test_a_new_cache_may_be_used_on_any_stream_at_once():
+    """The constructor's zeros are in place when it returns: a row written on
+    another stream right away stays."""
+    x, s = _randn(_gen(1), 1, 8, 128), torch.cuda.Stream()
+    warm = tq.PagedCache(1, 8, 128, page_size=64)
+    slots = torch.zeros(1, dtype=torch.int64, device=DEV)
+    warm.write(x, x, slots, stored=True, stream=s)
+    room = torch.empty(3 << 30, dtype=torch.uint8, device=DEV)       # two pools of 1 GB come from what this leaves
+    del room
+    last = slots + 30000 * 64 - 1
+    torch.cuda.synchronize()
+    cache = tq.PagedCache(30000, 8, 128, page_size=64)
+    ks, vs = cache.write(x, x, last, stored=True, stream=s)
+    torch.cuda.synchronize()
+    kr, vr = cache.read(last, dtype=torch.float32)
+    assert torch.equal(kr, ks) and torch.equal(vr, vs)
