@@ -492,16 +492,17 @@ tq_status tq_paged_read(tq_paged *ctx, const tq_pages *pages, const int64_t *slo
  *               arguments.
  * Tokens that no query sees may hold anything.  A length outside
  * [0, max_pages * page_size], a query start outside [0, total_q] or a
- * decreasing one is held to those bounds, tokens of a page number outside the
- * pool are not seen, and each sets error flag bit 1 in the status word.
+ * decreasing one is held to those bounds (rows that two sequences then claim
+ * are undefined), tokens of a page number outside the pool are not seen, and
+ * each sets error flag bit 1 in the status word.
  * n_q_heads <= TQ_MAX_HEADS, batch <= TQ_MAX_PAGED_SEQS, and total_q *
  * n_q_heads and max_pages * page_size below 2^30 (TQ_ERR_LIMIT).  Up to two
  * kernels: few rows of a kv head (its queries times the query heads that share
  * it: 48 at d = 64, 32 at 128, 16 at 256) are multiplied as register
  * fragments, more on the tcgen05 tensor cores; the second kernel joins the
- * sequences that were split, where there can be such.  Results do not depend on the other sequences'
- * contents, but on how a call's work is split, that is on its shapes and
- * lengths, in the last bits. */
+ * sequences that were split, where there can be such.  Results do not depend
+ * on the other sequences' contents, but on how a call's work is split, that is
+ * on its shapes and lengths, in the last bits. */
 size_t tq_paged_workspace_bytes(const tq_paged *ctx, int n_q_heads, int n_kv_heads, int batch, int64_t max_pages,
                                 int max_q_len);
 tq_status tq_paged_attention(tq_paged *ctx, const tq_pages *pages, const void *q, tq_dtype dtype, int64_t total_q,

@@ -638,8 +638,10 @@ class PagedCache:
         and the end (None: one query per sequence); max_q_len: the most
         queries of a sequence, as a hint (default their mean);
         window: 0, or how many tokens back a query sees besides the first
-        `sinks`; scale: positive (default 1/sqrt(head_dim)).  Returns `out` (like q;
-        rows of no sequence are not written)."""
+        `sinks`; scale: positive (default 1/sqrt(head_dim)).  Entries of
+        pages of which no query sees a token are not read, and tokens that no
+        query sees may hold anything.  Returns `out` (like q, not overlapping
+        it; rows of no sequence are not written)."""
         if not self._here(stream):
             return self._elsewhere(stream, self.attention, q, page_table, seq_lens, q_starts, max_q_len, window, sinks,
                                    scale, out, workspace)

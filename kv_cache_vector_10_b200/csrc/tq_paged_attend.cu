@@ -9,15 +9,17 @@
 // and is used by few rows (queries times query heads of the group), so the
 // floor is the time to read the visible tokens.  At HBM rate an SM has about
 // 94 cycles for 16 tokens, that is some 370 warp instructions to turn 4096
-// codes into operands, multiply and take the softmax; it takes about 290,
+// codes into operands, multiply and take the softmax; it takes about 285,
 // issued at 0.6 a cycle and scheduler whether 8 or 12 warps are on an SM (the
-// integer pipe, which splices the codes, is the busiest, at 44%).  So a long
-// cache streams at 79% of the copy rate (each further 2^21 tokens of a kv
-// head 55 us, 285 MB), and a call costs about 9 us beside that: its start, the
-// shares, the first tiles' way from memory, the last's way through the warps,
-// and the join.  4 sequences of 32768 tokens, 8 kv heads, 32 query heads, d =
-// 128 (143 MB): 42 us, 51% of the copy rate; one sequence of 1024 tokens and
-// 8 kv heads, not split: 11 us, as long as its host work.  Hence:
+// integer pipe, which splices the codes, is the busiest, at 40%).  So each
+// further 2^21 tokens of a kv head take 56 us at d = 128 (285 MB, 78% of the
+// copy rate; d = 64: 37 us, 59%; d = 256: 119 us, 73%).  The line through
+// calls of 2^18 to 2^21 tokens meets none at 13 us (d = 256: 19): a call of
+// one tile an item takes 9.4 us (start, shares, the first tiles' way from
+// memory, the last's way through the warps, the join), and the rest of the
+// line's start has not been taken apart.  4 sequences of 32768 tokens, 8 kv
+// heads, 32 query heads, d = 128 (143 MB): 41 us, 53% of the copy rate; one
+// sequence of 1024 tokens and one kv head, not split: 10.3 us.  Hence:
 //   * codes go from shared memory into registers as the fragments of
 //     mma.m16n8k16 (tokens or channels as the 16 rows, queries as the 8
 //     columns) and are widened there: no operand is written back to shared
@@ -60,7 +62,9 @@ struct Cfg {
     static constexpr int NST = D == 64 ? 3 : 2;                // stages: a tile for each warp
     // CTAs of an SM: as many as the registers of the fragments allow (a third
     // one at d = 128, NT = 1 takes 48 us instead of 43.5 for 4 x 32768 tokens
-    // and 22.1 instead of 20.0 for 4 x 8192)
+    // and 22.1 instead of 20.0 for 4 x 8192).  d = 128, NT = 1 spills none of
+    // them; the others do (stores and loads in bytes: d = 64, NT = 1 36 and 44,
+    // NT = 2 288 and 372; d = 128, NT = 2 492 and 564; d = 256 204 and 276).
     static constexpr int CTAS = D == 64 ? 4 - NT / 2 : 2;
     using Load = TileLoad<D, TT, NW>;
     static constexpr int SMEM = NST * Load::STAGE;
@@ -526,7 +530,8 @@ tq_status launch_decode(PagedAttn P, int64_t rows, int n_sms, cudaStream_t strea
     // a part of a round takes as long as a whole one (in single tiles: 8 x 4096
     // tokens of 32 kv heads 45.0 us instead of 43.6, drafted tokens 18.6
     // instead of 17.1, 4 x 32768 the same, but 32 windows of 1024, short
-    // against a round, 23.6 instead of 24.6).  An item's queries and the join
+    // against a round, 23.6 instead of 24.6, and 8 x 4096 tokens at d = 256
+    // 30.8 instead of 32.4).  An item's queries and the join
     // of its warps' parts take about a round (not counted: drafted tokens 18.6,
     // 4 x 32768 43.5 instead of 42.2, the others within 1%).
     P.item_cost = 1;
@@ -539,10 +544,10 @@ tq_status launch_decode(PagedAttn P, int64_t rows, int n_sms, cudaStream_t strea
     //     2      8.0  6.6  8.8  7.0   8.8  7.4  9.9  8.0  11.5  9.9 13.8 10.3
     //     4      8.2  8.8  9.7  9.2   8.9 10.3 12.0 10.7  11.1 12.9 15.8 13.4
     //     8      8.4 13.5 11.9 14.0   9.2 15.8 13.0 16.4  11.4 19.3 16.5 19.7
-    // and a call that is not replayed from a graph takes 15.8 cut, 11.3 to 13.4
-    // whole up to four rounds, 13.8 to 20.2 at eight.  So: whole up to four
+    // and a call that is not replayed from a graph takes about 16 cut, 11.3 to
+    // 13.8 whole up to four rounds, 13.8 to 20.2 at eight.  So: whole up to four
     // rounds, where a replayed step of few items loses up to 2.3 us (at four
-    // rounds) and every other call gains 1 to 4.5.
+    // rounds) and every other call gains 0.5 to 4.5.
     P.whole_tokens = 4 * NW * C::TT;
     const int64_t items = (int64_t)P.batch * P.Hkv * ((rows + R - 1) / R);
     const PagedGrid grid = tq_paged_grid(P, items, P.max_tokens / (C::TT * NW) + 1, n_sms * C::CTAS, R, D);

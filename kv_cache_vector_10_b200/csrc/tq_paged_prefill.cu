@@ -16,12 +16,18 @@
 // Roles: NM x 4 softmax warps, 4 (NM = 2) or 8 widening warps, one warp that
 // requests the codes (bulk copies of pages), one that issues the MMAs.
 // Measured: 2048 queries over 8192 tokens, 32 query heads on 8 kv heads, d =
-// 128: 270 us, 890 TFLOP/s, 54% of the cuBLAS burst rate.  A tile of both row
+// 128: 272 to 277 us on several boxes, 870 to 885 TFLOP/s, 53% of the cuBLAS
+// burst rate.  A tile of both row
 // blocks takes 2150 cycles, of which the tensor cores need 1024 at their best
 // and 1460 for products of 64 columns, shared memory some 1600 (the queries
 // are read from it) and each softmax warp 1800.  Whole prompts of 1674, 3127
 // and 4001 tokens under a window of 1024 with 4 sinks, 8 query heads on 2 kv
-// heads, d = 256: 114 us, 540 TFLOP/s.
+// heads, d = 256: 116 us, 530 TFLOP/s; tensor pipe 31% busy, integer pipe
+// 37%, issue slots 42%: the items are short (14.7 tiles), and between them the
+// tensor cores wait for the softmax warps, which also load the next queries
+// and store the rows.  Registers are spilled at every size (stores and loads
+// in bytes: NM = 2 404 and 504 at d = 128, 576 and 780 at d = 64; NM = 1 212
+// to 224 and 152 to 156).
 #include <algorithm>
 
 #include "tq_paged.cuh"
