@@ -183,3 +183,36 @@ def test_a_new_cache_may_be_used_on_any_stream_at_once():
     torch.cuda.synchronize()
     kr, vr = cache.read(last, dtype=torch.float32)
     assert torch.equal(kr, ks) and torch.equal(vr, vs)
+
+
+# ------------------------------------------------------- division of the work
+
+@pytest.mark.parametrize("d,B,H", [(64, 290, 2), (64, 592, 1), (128, 290, 1), (128, 37, 8), (256, 296, 1), (64, 593, 1)])
+@pytest.mark.parametrize("most", [1, 4])
+def test_short_sequences_with_a_cta_each(d, B, H, most):
+    """No more sequences and kv heads than CTAs, of unlike lengths, some empty
+    or without queries; too few queries announced (more items than CTAs then)."""
+    lens = [(37 * i) % 480 for i in range(B)]
+    new = [min(lens[i], (i % 7 == 0) * 30 + i % 5) for i in range(B)]
+    starts = np.concatenate(([0], np.cumsum(new)))
+    cache, table, lens_t, g = _pool(lens, H, d, 16, seed=d + B)
+    assert cache.workspace_bytes(4 * H, B, table.shape[1], most) == 0
+    q = _randn(g, int(starts[-1]) + 2, 4 * H, d, dtype=torch.float16)
+    out = torch.full_like(q, 7.0)
+    st = torch.tensor(starts, dtype=torch.int32, device=DEV)
+    cache.attention(q, table, lens_t, q_starts=st, max_q_len=most, out=out, window=300, sinks=3)
+    _check(cache, q, table, lens_t, starts, out, window=300, sinks=3)
+    assert (out[int(starts[-1]):] == 7.0).all() and cache.status() == (0, 0)
+
+
+@pytest.mark.parametrize("d,B,H", [(64, 18, 8), (128, 36, 4), (256, 70, 2)])
+def test_short_prompts_with_a_cta_each(d, B, H):
+    lens = [(37 * i) % 62 for i in range(B)]
+    starts = np.concatenate(([0], np.cumsum(lens)))
+    cache, table, lens_t, g = _pool(lens, H, d, 32, seed=d + B)
+    q = _randn(g, int(starts[-1]), 2 * H, d, dtype=torch.bfloat16)
+    st = torch.tensor(starts, dtype=torch.int32, device=DEV)
+    for most in (62, 30):
+        out = cache.attention(q, table, lens_t, q_starts=st, max_q_len=most)
+        _check(cache, q, table, lens_t, starts, out)
+    assert cache.status() == (0, 0)
