@@ -15,7 +15,7 @@
 // further 2^21 tokens of a kv head take 56 us at d = 128 (285 MB, 78% of the
 // copy rate; d = 64: 37 us, 59%; d = 256: 119 us, 73%).  The line through
 // calls of 2^18 to 2^21 tokens meets none at 13 us (d = 256: 19): a call of
-// one tile an item takes 9.4 us (start, shares, the first tiles' way from
+// one round an item takes 9.4 us (start, shares, the first tiles' way from
 // memory, the last's way through the warps, the join), and the rest of the
 // line's start has not been taken apart.  4 sequences of 32768 tokens, 8 kv
 // heads, 32 query heads, d = 128 (143 MB): 41 us, 53% of the copy rate; one
@@ -546,8 +546,10 @@ tq_status launch_decode(PagedAttn P, int64_t rows, int n_sms, cudaStream_t strea
     //     8      8.4 13.5 11.9 14.0   9.2 15.8 13.0 16.4  11.4 19.3 16.5 19.7
     // and a call that is not replayed from a graph takes about 16 cut, 11.3 to
     // 13.8 whole up to four rounds, 13.8 to 20.2 at eight.  So: whole up to four
-    // rounds, where a replayed step of few items loses up to 2.3 us (at four
-    // rounds) and every other call gains 0.5 to 4.5.
+    // rounds, where calls gain 2 to 5 us, and a replayed step of few items loses
+    // up to 2.3 us (at four rounds).  Of 768 items, more than the CTAs, whole
+    // ones are the faster at up to two rounds; at four they take 27.6 us where
+    // cut 26.1 (d = 64), 36.9 and 37.5 (128), 47.6 and 51.7 (256).
     P.whole_tokens = 4 * NW * C::TT;
     const int64_t items = (int64_t)P.batch * P.Hkv * ((rows + R - 1) / R);
     const PagedGrid grid = tq_paged_grid(P, items, P.max_tokens / (C::TT * NW) + 1, n_sms * C::CTAS, R, D);
